@@ -82,6 +82,13 @@ enum {
     MOE_FMT_INT2_ROWSCALE = 3    /* int2 codes + fp32 scale per output row */
 };
 
+/* element types of the rows that the token-sorting and adapter calls take */
+enum {
+    MOE_DTYPE_F16 = 0,           /* fp16 */
+    MOE_DTYPE_BF16 = 1,          /* bfloat16 */
+    MOE_DTYPE_F32 = 2            /* fp32 */
+};
+
 /* Shape and hyper-parameters of one layer. */
 typedef struct moe_layer_desc {
     int hidden;            /* H: model width, fan-in of gate/up, fan-out of down */
@@ -236,6 +243,67 @@ int moe_expert_ffn(const moe_layer *layer, const uint16_t *x, int T, const int32
 int moe_combine(const moe_layer *layer, const float *y_assign, const float *y_shared,
                 const float *topk_w, int T, uint16_t *y, moe_stream_t stream);
 
+/* ---------------------------------------------------------------- sorted rows */
+
+/* Tokens sorted by expert and back, for experts that run outside this library (experts
+ * under training, a grouped product over tiles of rows, experts on another device): the
+ * rows themselves, where moe_group gives index lists and moe_expert_ffn gathers inside.
+ * Source: the grouping is the batch MoE union of moe_group; the pages move no rows.
+ *
+ * Sorted rows are a row-major array [n_rows][H] without gaps between rows.  The rows of
+ * expert e start at seg_offsets[e], a multiple of `align`; counts[e] of them are tokens, in
+ * ascending assignment order a = t*k + j, the rest up to seg_offsets[e + 1] is padding.
+ * row_of[a] is the row of assignment a, or -1 for an entry that topk_idx drops (-1).
+ * `dtype` arguments are MOE_DTYPE_*; row strides (ld*) count elements, are at least H and
+ * keep every row 16-byte aligned; base pointers are 16-byte aligned.  Outputs may not
+ * overlap inputs.  These calls use the current device, which must be the handle's
+ * (MOE_ERR_INVALID_ARG otherwise); sums are held in fp32 and rounded once. */
+
+/* Rows that hold the sorted rows of any T tokens: T*k + min(E, T*k) * (align - 1); 0 if T is
+ * out of [0, max_tokens] or align out of [1, 1024].  A pure host function. */
+size_t moe_sorted_rows(const moe_layer *layer, int T, int align);
+
+/* Bytes of workspace moe_sort_tokens needs for T tokens (0 if T is out of range); the
+ * workspace of moe_workspace_size(layer, T) serves as well (its counters stay zero). */
+size_t moe_sort_workspace_size(const moe_layer *layer, int T);
+
+/* Sorts T tokens by expert.  topk_idx int32 [T][k] as moe_route writes it (-1: dropped;
+ * other values outside [0, E) set MOE_ERR_DEVICE_BOUNDS and are dropped).  Outputs: rows
+ * [n_rows][H] of x's type, row_of int32 [T*k], counts int32 [E], seg_offsets int32 [E + 1].
+ * n_rows is at least moe_sorted_rows(layer, T, align) (else MOE_ERR_WORKSPACE).  Padding rows
+ * below seg_offsets[E] are zeroed; rows from there on are left as they were.  A token is
+ * copied bit for bit.  1 <= align <= 1024; T = 0 writes counts and seg_offsets (zeros). */
+int moe_sort_tokens(const moe_layer *layer, const void *x, int dtype, int64_t ldx, const int32_t *topk_idx,
+                    int T, int align, void *rows, size_t n_rows, int32_t *row_of, int32_t *counts,
+                    int32_t *seg_offsets, void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Its gradient: dx[t] = sum_j drows[row_of[t*k + j]], j ascending, entries of -1 skipped
+ * (a token all of whose entries are dropped gets zeros).  drows [n_rows][H]; padding rows
+ * are not read.  Values of row_of outside [-1, n_rows) set MOE_ERR_DEVICE_BOUNDS and are
+ * skipped, here and in the two calls below. */
+int moe_sort_tokens_backward(const moe_layer *layer, const void *drows, int rows_dtype, size_t n_rows,
+                             const int32_t *row_of, int T, void *dx, int dx_dtype, int64_t lddx,
+                             moe_stream_t stream);
+
+/* Sorted rows back to tokens, weighted: y[t] = y_shared[t] + sum_j topk_w[t][j] *
+ * rows[row_of[t*k + j]], summed in moe_combine's order (shared, j = 0 .. k-1); entries of -1
+ * and entries of weight 0 are skipped.  topk_w fp32 [T][k]; y_shared fp32 [T][H] or NULL. */
+int moe_unsort_tokens(const moe_layer *layer, const void *rows, int rows_dtype, size_t n_rows,
+                      const int32_t *row_of, const float *topk_w, const float *y_shared, int T, void *y,
+                      int y_dtype, int64_t ldy, moe_stream_t stream);
+
+/* Its gradient: drows[row_of[a]] = topk_w[a] * dy[t] (a = t*k + j; zeros for weight 0, whose
+ * row the forward pass skips) and dw[a] = sum_h dy[t][h] * rows[row_of[a]][h], fp32 [T*k] (0
+ * for entries of -1).  drows has the type of rows; y_shared's gradient is dy.  counts and
+ * seg_offsets (both, as moe_sort_tokens wrote them) make the call zero the padding rows of
+ * drows; with both NULL they are left as they were, as are rows behind the last segment.
+ * A row that two entries name is written by both in no fixed order: row_of names each row
+ * once at most. */
+int moe_unsort_tokens_backward(const moe_layer *layer, const void *dy, int dy_dtype, int64_t lddy,
+                               const void *rows, int rows_dtype, size_t n_rows, const int32_t *row_of,
+                               const float *topk_w, const int32_t *counts, const int32_t *seg_offsets, int T,
+                               void *drows, float *dw, moe_stream_t stream);
+
 /* ---------------------------------------------------------------- fused layer */
 
 /* Source: the whole MoE layer with routing fused into the small-batch kernels (648news
@@ -278,6 +346,82 @@ int moe_forward_fused(const moe_layer *layer, const uint16_t *x, int T, uint16_t
  * workspace must be ordered (the same stream, or one capture sequence). */
 int moe_forward_host(const moe_layer *layer, const uint16_t *x_host, int T, uint16_t *y_host,
                      void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* ---------------------------------------------------------------- low-rank adapters */
+
+/* Low-rank adapters of many requests beside one shared projection: every token names the
+ * adapter of its request, and y[t] = y_in[t] + scaling[a] * B_a (A_a x[t]).  Beside the layer:
+ * on the router's logits (moe_route's logits_out, then logits_in) and on the shared
+ * expert's fp32 output (y_shared, before moe_combine), or on any projection outside it.
+ * Source: the pages serve several users at once from one set of quantised weights (648news
+ * GLM-5.3-Flash vLLM page, section "OpenAI互換APIで動く320BパラメータのMoE構成"); they name no
+ * adapters. */
+
+/* Shape of a pool of adapters of one projection. */
+typedef struct moe_adapters_desc {
+    int in_features;       /* K: 8 .. 16384, a multiple of 8 */
+    int out_features;      /* N: 1 .. 16384 */
+    int n_adapters;        /* 1 .. 1024 */
+    int max_rank;          /* R: 8 .. 128, a multiple of 8 */
+    int dtype;             /* MOE_DTYPE_F16 or MOE_DTYPE_BF16: type of A, B, x and dy */
+    int max_tokens;        /* largest T any call on this handle will pass, 1 .. 65536 */
+} moe_adapters_desc;
+
+/* Device pointers to the pool's parameters (borrowed, 16-byte aligned; their values may
+ * change between calls):
+ *   a [n_adapters][R][K], b [n_adapters][N][R] in the pool's type, scaling fp32 [n_adapters],
+ *   rank int32 [n_adapters] in [0, R], or NULL: every adapter has rank R.
+ * Rows of a and columns of b from an adapter's rank on are never used (they may hold
+ * anything).  Ranks outside [0, R] set MOE_ERR_DEVICE_BOUNDS and count as 0. */
+typedef struct moe_adapters_weights {
+    const void *a, *b;
+    const float *scaling;
+    const int32_t *rank;
+} moe_adapters_weights;
+
+typedef struct moe_adapters moe_adapters;   /* opaque handle */
+
+/* Validates desc and weights and builds the handle on the current device (a device status
+ * word is its only allocation).  Returns MOE_OK and *out, or an error code and *out = NULL.
+ * Calls on the handle use the current device, which must be the handle's. */
+int moe_adapters_create(const moe_adapters_desc *desc, const moe_adapters_weights *weights, moe_adapters **out);
+
+/* Frees the handle; no call on it may still be running.  NULL is accepted. */
+int moe_adapters_destroy(moe_adapters *adapters);
+
+/* Bytes of device workspace a call with T tokens needs (0 if T is out of range), 256-byte
+ * aligned, not used by two calls that may run concurrently.  It needs no initial value. */
+size_t moe_adapters_workspace_size(const moe_adapters *adapters, int T);
+
+/* y[t] = y_in[t] + scaling[a] * B_a (A_a x[t]), a = adapter_of[t], in fp32 with one rounding
+ * to y's type.  x [T][K] in the pool's type, rows 16-byte aligned (ldx counts elements, a
+ * multiple of 8); adapter_of int32 [T], -1: no adapter (other values outside
+ * [0, n_adapters) set MOE_ERR_DEVICE_BOUNDS and count as -1).  y [T][N] of type y_dtype
+ * (MOE_DTYPE_*), y_in of the same type (NULL: zeros; y itself: in place; otherwise it may not
+ * overlap y), any element alignment.  A token without an adapter gets y_in's bits.  z, if not
+ * NULL, receives A_a x[t] (fp32 [T][R], 16-byte aligned, zeros from the adapter's rank on and
+ * for tokens without an adapter), which the gradient needs. */
+int moe_adapters_apply(const moe_adapters *adapters, const void *x, int64_t ldx, const int32_t *adapter_of, int T,
+                       const void *y_in, int64_t ldy_in, void *y, int y_dtype, int64_t ldy, float *z,
+                       void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* Its gradient, given x, z as the forward call wrote it, and dy [T][N] in the pool's type
+ * (N a multiple of 8, rows 16-byte aligned).  With dz[t] = scaling[a] * B_a^T dy[t]:
+ *   dx[t] = dx_in[t] + A_a^T dz[t]   (dx [T][K] of type dx_dtype, dx_in of the same type, with
+ *                                     y's rules; dx = NULL: not computed)
+ *   da[a] = sum over a's tokens of dz[t] x[t]^T           (fp32 [n_adapters][R][K])
+ *   db[a] = sum over a's tokens of scaling[a] dy[t] z[t]^T   (fp32 [n_adapters][N][R])
+ * da and db, both or neither (NULL), 16-byte aligned.  accumulate = 0: every element is
+ * written, zeros where the batch has no token or from the adapter's rank on;
+ * accumulate = 1: the sums are added to what is there, and adapters without a token are
+ * left as they were.  y_in's gradient is dy.  T = 0 with accumulate = 0 writes zeros. */
+int moe_adapters_backward(const moe_adapters *adapters, const void *x, int64_t ldx, const float *z, const void *dy,
+                          int64_t lddy, const int32_t *adapter_of, int T, const void *dx_in, int64_t lddx_in,
+                          void *dx, int dx_dtype, int64_t lddx, float *da, float *db, int accumulate,
+                          void *workspace, size_t workspace_bytes, moe_stream_t stream);
+
+/* moe_get_device_status of an adapter handle. */
+int moe_adapters_get_device_status(const moe_adapters *adapters, int *status);
 
 /* ---------------------------------------------------------------- diagnostics */
 

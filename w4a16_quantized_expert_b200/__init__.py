@@ -25,6 +25,9 @@ MOE_FMT_INT4_ROWSCALE = 0
 MOE_FMT_NVFP4 = 1
 MOE_FMT_INT8_ROWSCALE = 2
 MOE_FMT_INT2_ROWSCALE = 3
+MOE_DTYPE_F16 = 0
+MOE_DTYPE_BF16 = 1
+MOE_DTYPE_F32 = 2
 MOE_PLAN_DECODE = 0
 MOE_PLAN_F16_BATCH = 1
 MOE_PLAN_TENSOR_MEMORY = 2
@@ -58,6 +61,15 @@ class moe_weights(ctypes.Structure):
 class moe_ws_routing(ctypes.Structure):
     _fields_ = [(f, c_size) for f in ("logits", "topk_idx", "topk_w", "counts", "offsets", "perm", "unique",
                                       "n_unique")]
+
+
+class moe_adapters_desc(ctypes.Structure):
+    _fields_ = [("in_features", c_int), ("out_features", c_int), ("n_adapters", c_int), ("max_rank", c_int),
+                ("dtype", c_int), ("max_tokens", c_int)]
+
+
+class moe_adapters_weights(ctypes.Structure):
+    _fields_ = [("a", vp), ("b", vp), ("scaling", vp), ("rank", vp)]
 
 
 class MoeError(RuntimeError):
@@ -99,6 +111,28 @@ def lib():
         L.moe_debug_wait_timeout.argtypes = [vp, ctypes.c_longlong, vp]
         L.moe_workspace_routing.argtypes = [vp, c_int, ctypes.POINTER(moe_ws_routing)]
         L.moe_plan.argtypes = [ctypes.POINTER(moe_layer_desc), c_int, ctypes.POINTER(c_int)]
+        i64 = ctypes.c_int64
+        L.moe_sorted_rows.argtypes = [vp, c_int, c_int]
+        L.moe_sort_workspace_size.argtypes = [vp, c_int]
+        L.moe_sort_tokens.argtypes = [vp, vp, c_int, i64, vp, c_int, c_int, vp, c_size, vp, vp, vp, vp, c_size, vp]
+        L.moe_sort_tokens_backward.argtypes = [vp, vp, c_int, c_size, vp, c_int, vp, c_int, i64, vp]
+        L.moe_unsort_tokens.argtypes = [vp, vp, c_int, c_size, vp, vp, vp, c_int, vp, c_int, i64, vp]
+        L.moe_unsort_tokens_backward.argtypes = [vp, vp, c_int, i64, vp, c_int, c_size, vp, vp, vp, vp, c_int, vp,
+                                                 vp, vp]
+        L.moe_adapters_create.argtypes = [ctypes.POINTER(moe_adapters_desc), ctypes.POINTER(moe_adapters_weights),
+                                          ctypes.POINTER(vp)]
+        L.moe_adapters_destroy.argtypes = [vp]
+        L.moe_adapters_workspace_size.argtypes = [vp, c_int]
+        L.moe_adapters_apply.argtypes = [vp, vp, i64, vp, c_int, vp, i64, vp, c_int, i64, vp, vp, c_size, vp]
+        L.moe_adapters_backward.argtypes = [vp, vp, i64, vp, vp, i64, vp, c_int, vp, i64, vp, c_int, i64, vp, vp,
+                                            c_int, vp, c_size, vp]
+        L.moe_adapters_get_device_status.argtypes = [vp, ctypes.POINTER(c_int)]
+        for f in ("moe_sorted_rows", "moe_sort_workspace_size", "moe_adapters_workspace_size"):
+            getattr(L, f).restype = c_size
+        for f in ("moe_sort_tokens", "moe_sort_tokens_backward", "moe_unsort_tokens", "moe_unsort_tokens_backward",
+                  "moe_adapters_create", "moe_adapters_destroy", "moe_adapters_apply", "moe_adapters_backward",
+                  "moe_adapters_get_device_status"):
+            getattr(L, f).restype = c_int
         for f in ("moe_layer_create", "moe_layer_destroy", "moe_route", "moe_route_static", "moe_group",
                   "moe_expert_ffn", "moe_combine", "moe_forward", "moe_forward_fused", "moe_forward_host", "moe_forward_timed",
                   "moe_get_device_status", "moe_debug_wait_timeout", "moe_workspace_routing", "moe_plan"):
@@ -206,3 +240,65 @@ def moe_workspace_routing(layer, T) -> dict:
     r = moe_ws_routing()
     _check(lib().moe_workspace_routing(layer, T, ctypes.byref(r)), "moe_workspace_routing")
     return {f: getattr(r, f) for f, _ in moe_ws_routing._fields_}
+
+
+def moe_sorted_rows(layer, T, align=1) -> int:
+    return lib().moe_sorted_rows(layer, T, align)
+
+
+def moe_sort_workspace_size(layer, T) -> int:
+    return lib().moe_sort_workspace_size(layer, T)
+
+
+def moe_sort_tokens(layer, x, dtype, ldx, topk_idx, T, align, rows, n_rows, row_of, counts, seg_offsets, ws, ws_bytes,
+                    stream=0):
+    _check(lib().moe_sort_tokens(layer, x, dtype, ldx, topk_idx, T, align, rows, n_rows, row_of, counts, seg_offsets,
+                                 ws, ws_bytes, stream), "moe_sort_tokens")
+
+
+def moe_sort_tokens_backward(layer, drows, rows_dtype, n_rows, row_of, T, dx, dx_dtype, lddx, stream=0):
+    _check(lib().moe_sort_tokens_backward(layer, drows, rows_dtype, n_rows, row_of, T, dx, dx_dtype, lddx, stream),
+           "moe_sort_tokens_backward")
+
+
+def moe_unsort_tokens(layer, rows, rows_dtype, n_rows, row_of, topk_w, y_shared, T, y, y_dtype, ldy, stream=0):
+    _check(lib().moe_unsort_tokens(layer, rows, rows_dtype, n_rows, row_of, topk_w, y_shared, T, y, y_dtype, ldy,
+                                   stream), "moe_unsort_tokens")
+
+
+def moe_unsort_tokens_backward(layer, dy, dy_dtype, lddy, rows, rows_dtype, n_rows, row_of, topk_w, counts,
+                               seg_offsets, T, drows, dw, stream=0):
+    _check(lib().moe_unsort_tokens_backward(layer, dy, dy_dtype, lddy, rows, rows_dtype, n_rows, row_of, topk_w,
+                                            counts, seg_offsets, T, drows, dw, stream), "moe_unsort_tokens_backward")
+
+
+def moe_adapters_create(desc: moe_adapters_desc, weights: moe_adapters_weights) -> int:
+    h = vp()
+    _check(lib().moe_adapters_create(ctypes.byref(desc), ctypes.byref(weights), ctypes.byref(h)),
+           "moe_adapters_create")
+    return h.value
+
+
+def moe_adapters_destroy(adapters: int) -> None:
+    _check(lib().moe_adapters_destroy(adapters), "moe_adapters_destroy")
+
+
+def moe_adapters_workspace_size(adapters: int, T: int) -> int:
+    return lib().moe_adapters_workspace_size(adapters, T)
+
+
+def moe_adapters_apply(adapters, x, ldx, adapter_of, T, y_in, ldy_in, y, y_dtype, ldy, z, ws, ws_bytes, stream=0):
+    _check(lib().moe_adapters_apply(adapters, x, ldx, adapter_of, T, y_in, ldy_in, y, y_dtype, ldy, z, ws, ws_bytes,
+                                    stream), "moe_adapters_apply")
+
+
+def moe_adapters_backward(adapters, x, ldx, z, dy, lddy, adapter_of, T, dx_in, lddx_in, dx, dx_dtype, lddx, da, db,
+                          accumulate, ws, ws_bytes, stream=0):
+    _check(lib().moe_adapters_backward(adapters, x, ldx, z, dy, lddy, adapter_of, T, dx_in, lddx_in, dx, dx_dtype,
+                                       lddx, da, db, accumulate, ws, ws_bytes, stream), "moe_adapters_backward")
+
+
+def moe_adapters_get_device_status(adapters) -> int:
+    st = c_int(0)
+    _check(lib().moe_adapters_get_device_status(adapters, ctypes.byref(st)), "moe_adapters_get_device_status")
+    return st.value

@@ -10,8 +10,19 @@
 #include <new>
 
 #include "moe_internal.h"
+#include "moe_rows.cuh"
 
 namespace moe {
+cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k, int E, int align,
+                             void *rows, const int32_t *row_of, const int32_t *counts, const int32_t *seg,
+                             int num_sms, cudaStream_t s);
+cudaError_t launch_unsort(const void *rows, int rows_dtype, int n_rows, const int32_t *row_of, const float *w, int T,
+                          int k, int H, const float *shared, void *y, int y_dtype, long long ldy, int *status,
+                          int num_sms, cudaStream_t s);
+cudaError_t launch_unsort_grad(const void *dy, int dy_dtype, long long lddy, const void *rows, int rows_dtype,
+                               int n_rows, const int32_t *row_of, const float *w, const int32_t *counts,
+                               const int32_t *seg, int T, int k, int H, int E, void *drows, float *dw, int *status,
+                               int num_sms, cudaStream_t s);
 cudaError_t launch_router(const RouterParams &p, bool pdl, cudaStream_t s);
 cudaError_t router_prepare();
 cudaError_t launch_group(const GroupParams &p, cudaStream_t s);
@@ -228,6 +239,33 @@ int check_ws(const moe_layer *L, int T, void *ws, size_t bytes)
 }
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// ------------------------------------------------------------------ sorted rows
+constexpr int kMaxAlign = 1024;
+
+size_t dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
+bool known_dtype(int dtype) { return dtype >= MOE_DTYPE_F16 && dtype <= MOE_DTYPE_F32; }
+
+// rows of `width` elements, `ld` apart, every one 16-byte aligned
+bool rows_ok(const void *p, int dtype, int width, int64_t ld)
+{
+    return p && known_dtype(dtype) && aligned16(p) && ld >= width && (uint64_t)ld < (1ull << 40) &&
+           (size_t)ld * dtype_bytes(dtype) % 16 == 0;
+}
+
+bool on_device(int device)
+{
+    int d = -1;
+    return cudaGetDevice(&d) == cudaSuccess && d == device;
+}
+
+// scratch of the sort: behind the counter block, so that a layer's workspace serves and its
+// counters stay zero
+size_t sort_ws_bytes(const moe_layer_desc &d, int T)
+{
+    const size_t chunks = ((size_t)T * d.top_k + kSortChunk - 1) / kSortChunk;
+    return ws_layout(d, 0).ctr_end + up256(chunks * d.n_experts * 4);
+}
 
 
 LayerWeights layer_weights(const moe_layer *L)
@@ -693,6 +731,93 @@ int moe_combine(const moe_layer *L, const float *y_assign, const float *y_shared
     p.k = L->desc.top_k;
     p.n_shared = L->desc.n_shared;
     return cuda_status(launch_combine(p, false, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_sorted_rows(const moe_layer *L, int T, int align)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens || align < 1 || align > kMaxAlign) return 0;
+    const size_t n = (size_t)T * L->desc.top_k;
+    return n + std::min<size_t>(L->desc.n_experts, n) * (align - 1);
+}
+
+size_t moe_sort_workspace_size(const moe_layer *L, int T)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens) return 0;
+    return sort_ws_bytes(L->desc, T);
+}
+
+int moe_sort_tokens(const moe_layer *L, const void *x, int dtype, int64_t ldx, const int32_t *topk_idx, int T,
+                    int align, void *rows, size_t n_rows, int32_t *row_of, int32_t *counts, int32_t *seg_offsets,
+                    void *ws, size_t ws_bytes, moe_stream_t stream)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens || align < 1 || align > kMaxAlign) return MOE_ERR_INVALID_ARG;
+    const moe_layer_desc &d = L->desc;
+    if (!counts || !seg_offsets || !on_device(L->device)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!rows_ok(x, dtype, d.hidden, ldx) || !topk_idx || !row_of || !rows || !aligned16(rows)))
+        return MOE_ERR_INVALID_ARG;
+    if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u) || ws_bytes < sort_ws_bytes(d, T)) return MOE_ERR_WORKSPACE;
+    if (n_rows < moe_sorted_rows(L, T, align)) return MOE_ERR_WORKSPACE;
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    SortParams p = {};
+    p.key = topk_idx;
+    p.n = T * d.top_k;
+    p.E = d.n_experts;
+    p.align = align;
+    p.none_bin = -1;
+    p.counts = counts;
+    p.seg = seg_offsets;
+    p.row_of = row_of;
+    p.hist = at<int32_t>(ws, ws_layout(d, 0).ctr_end);
+    p.status = L->d_status;
+    const cudaError_t e = launch_sort(p, s);
+    if (e != cudaSuccess || T == 0) return cuda_status(e);
+    const size_t es = dtype_bytes(dtype);
+    return cuda_status(launch_sort_copy(x, (size_t)ldx * es, (size_t)d.hidden * es, T, d.top_k, d.n_experts, align,
+                                        rows, row_of, counts, seg_offsets, L->num_sms, s));
+}
+
+int moe_sort_tokens_backward(const moe_layer *L, const void *drows, int rows_dtype, size_t n_rows,
+                             const int32_t *row_of, int T, void *dx, int dx_dtype, int64_t lddx,
+                             moe_stream_t stream)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens || !on_device(L->device)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const int H = L->desc.hidden;
+    if (!rows_ok(drows, rows_dtype, H, H) || !row_of || !rows_ok(dx, dx_dtype, H, lddx) || n_rows > 0x7fffffffu)
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_unsort(drows, rows_dtype, (int)n_rows, row_of, nullptr, T, L->desc.top_k, H, nullptr, dx,
+                                     dx_dtype, lddx, L->d_status, L->num_sms,
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_unsort_tokens(const moe_layer *L, const void *rows, int rows_dtype, size_t n_rows, const int32_t *row_of,
+                      const float *topk_w, const float *y_shared, int T, void *y, int y_dtype, int64_t ldy,
+                      moe_stream_t stream)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens || !on_device(L->device)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const int H = L->desc.hidden;
+    if (!rows_ok(rows, rows_dtype, H, H) || !row_of || !topk_w || !aligned16(y_shared) ||
+        !rows_ok(y, y_dtype, H, ldy) || n_rows > 0x7fffffffu)
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_unsort(rows, rows_dtype, (int)n_rows, row_of, topk_w, T, L->desc.top_k, H, y_shared, y,
+                                     y_dtype, ldy, L->d_status, L->num_sms, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int moe_unsort_tokens_backward(const moe_layer *L, const void *dy, int dy_dtype, int64_t lddy, const void *rows,
+                               int rows_dtype, size_t n_rows, const int32_t *row_of, const float *topk_w,
+                               const int32_t *counts, const int32_t *seg_offsets, int T, void *drows, float *dw,
+                               moe_stream_t stream)
+{
+    if (!L || T < 0 || T > L->desc.max_tokens || !on_device(L->device)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    const int H = L->desc.hidden;
+    if (!rows_ok(dy, dy_dtype, H, lddy) || !rows_ok(rows, rows_dtype, H, H) || !row_of || !topk_w || !drows ||
+        !aligned16(drows) || !dw || !counts != !seg_offsets || n_rows > 0x7fffffffu)
+        return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_unsort_grad(dy, dy_dtype, lddy, rows, rows_dtype, (int)n_rows, row_of, topk_w, counts,
+                                          seg_offsets, T, L->desc.top_k, H, L->desc.n_experts, drows, dw, L->d_status,
+                                          L->num_sms, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int moe_forward(const moe_layer *L, const uint16_t *x, int T, uint16_t *y, void *ws, size_t ws_bytes,
