@@ -1,7 +1,21 @@
 // moe_adapters.cu -- low-rank adapters of many requests beside a shared projection, and
 // their gradients: kernels and entry points.
+//
+// y = y_in + s B (A x) per token is two thin products: the shrink z = A x contracts the long
+// axis and the expand adds s B z over it.  Both are bound by the rows of x and y (or, for a
+// few tokens, by the adapters' weights and launch latency) as long as the products run on
+// the tensor cores.  Batches of at most 32 tokens take two latency-sized kernels
+// (shrink_few_kernel, expand_few_kernel); larger ones are sorted by adapter into tiles of
+// 128 tokens and take the tcgen05 kernels (shrink_tile_kernel, expand_tile_kernel,
+// grad_tile_kernel), and so does every gradient.
+//
+// z enters a second product, whose operands are 16-bit.  It is carried as two pieces
+// hi = T(z c), lo = T(z c - hi) with a power of two c per row (the gradient of the weights:
+// per adapter) that keeps fp16 in range: the product's error stays at fp32's level where a
+// single rounding of z to 16 bits would cost 2^-9 of the result.
 #include "moe_internal.h"
 #include "moe_rows.cuh"
+#include "moe_tcgen05.cuh"
 
 #include <algorithm>
 #include <new>
@@ -18,7 +32,14 @@ struct moe_adapters {
 namespace moe {
 namespace {
 
-constexpr int kAdThreads = 128;
+constexpr int kFewT = 32;          // tokens of the latency-sized path (one warp plans the batch)
+constexpr int kFewThreads = 128;
+constexpr int kFewK = 256;         // K values per CTA of the small shrink
+constexpr int kFewN = 128;         // columns per CTA of the small expand
+constexpr int kTile = 128;         // tokens per tile of the tcgen05 kernels (MMA M)
+constexpr int kBlk = kTile * 128;  // bytes of a [128 rows][64 columns] 16-bit block
+constexpr int kWorkers = 256;      // load and epilogue threads of a tcgen05 CTA
+constexpr int kMaxSplit = 8;       // CTAs of a cluster that share a contraction
 
 struct AdParams {
     const void *x, *dy;          // [T][K], [T][N] of the pool's type
@@ -26,162 +47,953 @@ struct AdParams {
     const float *scaling;
     const int32_t *rank, *adapter_of;
     const void *y_in;
-    void *y;
-    const float *zr;             // z read
-    float *z;                    // z or dz written
-    float *out;                  // da or db
+    void *y;                     // y, or dx
+    const float *z_in;           // z of the forward call (gradient)
+    float *z_out;                // optional z of this call
+    float *da, *db;
     long long ldx, lddy, ldy_in, ldy;
-    int T, K, N, R, n, accumulate;
+    int T, K, N, R, Kp, n, accumulate, want_dw;
+    // the plan: tokens sorted by adapter, tiles of 128 positions
+    int32_t *seg, *counts, *entry_of, *tile_bin;
+    // intermediates, by position: z (dz) as pieces [2 Kp], the scale that undoes c
+    void *limb, *zl, *dl;
+    float *row_scale, *dz;
+    unsigned *amax;              // [2][n] largest |dz|, |z| of each adapter (fp16 pools)
+    float *z_part;               // small path: [splits][T][R]
+    int splits;
     int *status;
 };
 
-__device__ __forceinline__ int adapter_at(const AdParams &p, int t)
+__device__ __forceinline__ int rank_of(const AdParams &p, int bin)
 {
-    const int a = p.adapter_of[t];
-    if (a >= 0 && a < p.n) return a;
-    if (a != -1) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
-    return -1;
-}
-
-__device__ __forceinline__ int rank_of(const AdParams &p, int a)
-{
+    if (bin >= p.n) return 0;
     if (!p.rank) return p.R;
-    const int r = p.rank[a];
+    const int r = __ldcg(p.rank + bin);
     if (r >= 0 && r <= p.R) return r;
     record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
     return 0;
 }
 
-// z[t][j] = sum_k x[t][k] A[j][k] (kGrad: dz[t][j] = s sum_n dy[t][n] B[n][j]): one CTA per
-// token and 8 ranks.
-template <typename TX, bool kGrad>
-__global__ void __launch_bounds__(kAdThreads) shrink_kernel(AdParams p)
+// the power of two that brings a largest magnitude m into [1, 4), and its inverse
+__device__ __forceinline__ float norm_scale(float m, float &inverse)
 {
-    __shared__ float red[kAdThreads / 32][8];
-    const int t = blockIdx.x, j0 = blockIdx.y * 8, tid = threadIdx.x;
-    pdl_trigger();
+    int e = static_cast<int>((__float_as_uint(m) >> 23) & 0xFFu);
+    e = min(max(e, 1), 253);
+    inverse = pow2f(e - 127);
+    return pow2f(127 - e);
+}
+
+__device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) <= 3.4028234663852886e38f ? fabsf(v) : 0.f; }
+
+// v as two pieces; an infinite or NaN piece stands alone
+template <typename T>
+__device__ __forceinline__ void split2(float v, T &hi, T &lo)
+{
+    hi = from_f32<T>(v);
+    const float h = f32_of(hi);
+    lo = from_f32<T>(fabsf(h) <= 3.4028234663852886e38f ? v - h : 0.f);
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ void mma_t(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                      uint32_t b1);
+template <>
+__device__ __forceinline__ void mma_t<__half>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1)
+{
+    mma_16816(c, a0, a1, a2, a3, b0, b1);
+}
+template <>
+__device__ __forceinline__ void mma_t<__nv_bfloat16>(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                                     uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// ============================================================================ few tokens
+// Tile `tile` of a batch of at most 32 tokens: up to 16 tokens of one adapter, in token
+// order.  One ballot per warp finds the tiles' first tokens.  Returns the adapter (n: tokens
+// without one), or -1 if there is no such tile; s_tok[0 .. cnt) receives the tokens.
+__device__ __forceinline__ int few_tile(const AdParams &p, int tile, int *s_tok, int &cnt)
+{
+    const int lane = threadIdx.x & 31;
+    int bin = -1 - lane;   // lanes without a token: alone in their group
+    if (lane < p.T) {
+        bin = __ldcg(p.adapter_of + lane);
+        if (bin < 0 || bin >= p.n) {
+            if (bin != -1) record_error(p.status, MOE_ERR_DEVICE_BOUNDS);
+            bin = p.n;
+        }
+    }
+    const unsigned below = (1u << lane) - 1u;
+    const unsigned same = __match_any_sync(0xffffffffu, bin);
+    const int at = __popc(same & below);
+    const unsigned first = __ballot_sync(0xffffffffu, bin >= 0 && at % 16 == 0);
+    const bool mine = bin >= 0 && at % 16 == 0 && __popc(first & below) == tile;
+    const unsigned who = __ballot_sync(0xffffffffu, mine);
+    if (!who) return -1;
+    const int lead = __ffs(who) - 1;
+    const int tile_bin = __shfl_sync(0xffffffffu, bin, lead), at0 = __shfl_sync(0xffffffffu, at, lead);
+    const bool in = bin == tile_bin && at >= at0 && at < at0 + 16;
+    cnt = __popc(__ballot_sync(0xffffffffu, in));
+    if (in && threadIdx.x < 32) s_tok[at - at0] = lane;
+    return tile_bin;
+}
+
+// z_part[split][t][j] = sum over the split's 256 K of x[t][k] A[j][k].  No shared-memory
+// staging: a thread's 16 bytes of a row are its operand of two m16n8k16 steps (the order of
+// K inside a product is free as long as both operands agree), so every load is issued up
+// front and the kernel is one memory latency long.  CTA (split, tile), 64 K per warp.
+template <typename TX, int NB>
+__global__ void __launch_bounds__(kFewThreads) shrink_few_kernel(const AdParams p)
+{
+    __shared__ int s_tok[16];
+    __shared__ float red[kFewThreads / 32][16][NB * 8 + 1];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
     pdl_wait();
-    const int a = adapter_at(p, t);
-    const int rank = a < 0 ? 0 : rank_of(p, a);
-    float acc[8] = {};
-    if (j0 < rank) {
-        if (kGrad) {
-            const TX *dy = static_cast<const TX *>(p.dy) + t * p.lddy;
-            const TX *B = static_cast<const TX *>(p.b) + (size_t)a * p.N * p.R;
-            for (int n = tid; n < p.N; n += kAdThreads) {
-                float f[8];
-                to_f32(load8(B + (size_t)n * p.R + j0), f);
-                const float d = f32_of(dy[n]);
+    pdl_trigger();   // (the expand kernel may now read what earlier grids wrote)
+    int cnt = 0;
+    const int bin = few_tile(p, blockIdx.y, s_tok, cnt);
+    if (bin < 0 || bin == p.n) return;
+    __syncthreads();
+    const TX *A = static_cast<const TX *>(p.a) + (size_t)bin * p.R * p.K;
+    const TX *x0 = static_cast<const TX *>(p.x) + (g < cnt ? s_tok[g] : 0) * p.ldx;
+    const TX *x1 = static_cast<const TX *>(p.x) + (g + 8 < cnt ? s_tok[g + 8] : 0) * p.ldx;
+    float acc[NB][4] = {};
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const int k0 = blockIdx.x * kFewK + warp * 64 + tig * 8;
+    constexpr int kU = NB > 8 ? 1 : 2;   // 32-K blocks whose loads are in flight together
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[i] = fmaf(d, f[i], acc[i]);
+    for (int b0 = 0; b0 < 2; b0 += kU) {
+        uint4 xa[kU], xb[kU], av[kU][NB];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int k = k0 + (b0 + u) * 32;
+            const bool in = k < p.K;
+            xa[u] = in && g < cnt ? *reinterpret_cast<const uint4 *>(x0 + k) : zero;
+            xb[u] = in && g + 8 < cnt ? *reinterpret_cast<const uint4 *>(x1 + k) : zero;
+#pragma unroll
+            for (int j = 0; j < NB; ++j)
+                av[u][j] = in && j * 8 + g < p.R
+                               ? *reinterpret_cast<const uint4 *>(A + (size_t)(j * 8 + g) * p.K + k) : zero;
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u)
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                mma_t<TX>(acc[j], xa[u].x, xb[u].x, xa[u].y, xb[u].y, av[u][j].x, av[u][j].y);
+                mma_t<TX>(acc[j], xa[u].z, xb[u].z, xa[u].w, xb[u].w, av[u][j].z, av[u][j].w);
             }
-        } else {
-            const TX *x = static_cast<const TX *>(p.x) + t * p.ldx;
-            const TX *A = static_cast<const TX *>(p.a) + ((size_t)a * p.R + j0) * p.K;
-            for (int k = tid * 8; k < p.K; k += kAdThreads * 8) {
-                float f[8], g[8];
-                to_f32(load8(x + k), f);
+    }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    to_f32(load8(A + (size_t)i * p.K + k), g);
+    for (int j = 0; j < NB; ++j) {
+        red[warp][g][j * 8 + 2 * tig] = acc[j][0];
+        red[warp][g][j * 8 + 2 * tig + 1] = acc[j][1];
+        red[warp][g + 8][j * 8 + 2 * tig] = acc[j][2];
+        red[warp][g + 8][j * 8 + 2 * tig + 1] = acc[j][3];
+    }
+    __syncthreads();
+    for (int i = tid; i < cnt * p.R; i += kFewThreads) {
+        const int row = i / p.R, j = i % p.R;
+        float v = red[0][row][j];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) acc[i] = fmaf(f[e], g[e], acc[i]);
+        for (int w = 1; w < kFewThreads / 32; ++w) v += red[w][row][j];
+        p.z_part[((size_t)blockIdx.x * p.T + s_tok[row]) * p.R + j] = v;
+    }
+}
+
+// y[t][n] = y_in[t][n] + s sum_j z[t][j] B[n][j] for 128 columns and a tile of up to 16
+// tokens.  B and y_in are loaded before the wait for the shrink kernel (which has itself
+// seen every earlier grid complete before this one may start), so after it only the
+// partial sums of z stand between the launch and the result.
+template <typename TX, typename TY, int KB>
+__global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams p)
+{
+    constexpr int W = KB * 16;
+    __shared__ int s_tok[16];
+    __shared__ float s_scale[16], s_z[16][W];
+    __shared__ __align__(8) TX s_hi[16][W], s_lo[16][W];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
+    pdl_trigger();
+    int cnt = 0;
+    const int bin = few_tile(p, blockIdx.y, s_tok, cnt);
+    if (bin < 0) {
+        pdl_wait();
+        return;
+    }
+    __syncthreads();
+    const int rank = rank_of(p, bin);
+    const int n0 = blockIdx.x * kFewN + warp * 32;
+    const TY *in = static_cast<const TY *>(p.y_in);
+    TY *y = static_cast<TY *>(p.y);
+    const int rows[2] = {g < cnt ? s_tok[g] : -1, g + 8 < cnt ? s_tok[g + 8] : -1};
+    if (rank == 0) {
+        pdl_wait();
+        if (p.z_out && blockIdx.x == 0)
+            for (int i = tid; i < cnt * p.R; i += kFewThreads) p.z_out[(size_t)s_tok[i / p.R] * p.R + i % p.R] = 0.f;
+        if (in == y) return;
+        for (int r = 0; r < cnt; ++r)   // the base's bits
+            if (n0 + lane < p.N)
+                y[s_tok[r] * p.ldy + n0 + lane] = in ? in[s_tok[r] * p.ldy_in + n0 + lane] : from_f32<TY>(0.f);
+        return;
+    }
+    const float scaling = __ldcg(p.scaling + bin);
+    const TX *B = static_cast<const TX *>(p.b) + (size_t)bin * p.N * p.R;
+    uint2 bv[4][KB];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int n = n0 + i * 8 + g;
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+            const int j = k * 16 + tig * 4;
+            bv[i][k] = make_uint2(0u, 0u);
+            if (n < p.N && j < rank) {   // (j < rank <= R: the four values are inside the row)
+                bv[i][k] = __ldcg(reinterpret_cast<const uint2 *>(B + (size_t)n * p.R + j));
+                if (j + 1 >= rank) bv[i][k].x &= 0xFFFFu;
+                if (j + 2 >= rank) bv[i][k].y = 0u;
+                else if (j + 3 >= rank) bv[i][k].y &= 0xFFFFu;
+            }
+        }
+    }
+    float yv[2][4][2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + i * 8 + tig * 2 + e;
+                yv[r][i][e] = in && rows[r] >= 0 && n < p.N ? f32_of(__ldcg(in + rows[r] * p.ldy_in + n)) : 0.f;
+            }
+    pdl_wait();
+    // z: the splits' sums, a few lanes per value when there are few values
+    {
+        const int n_el = cnt * p.R;
+        const int L = n_el <= 16 ? 8 : n_el <= 32 ? 4 : n_el <= 64 ? 2 : 1;
+        const int per = kFewThreads / L, part = tid % L;
+        for (int e0 = 0; e0 < n_el; e0 += per) {
+            const int e = e0 + tid / L;
+            float v = 0.f;
+            const int row = min(e, n_el - 1) / p.R, j = min(e, n_el - 1) % p.R;
+            const float *src = p.z_part + (size_t)s_tok[row] * p.R + j;
+#pragma unroll 8
+            for (int s = part; s < p.splits; s += L) v += __ldcg(src + (size_t)s * p.T * p.R);
+            for (int off = L >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+            if (e < n_el && part == 0) {
+                v = j < rank ? v : 0.f;
+                s_z[row][j] = v;
+                if (p.z_out && blockIdx.x == 0) p.z_out[(size_t)s_tok[row] * p.R + j] = v;
+            }
+        }
+    }
+    __syncthreads();
+    for (int row = warp; row < 16; row += kFewThreads / 32) {
+        float m = 0.f;
+        for (int j = lane; j < W; j += 32) m = fmaxf(m, row < cnt && j < p.R ? finite_or_0(s_z[row][j]) : 0.f);
+        float inv;
+        const float c = norm_scale(warp_max(m), inv);
+        for (int j = lane; j < W; j += 32) {
+            TX hi, lo;
+            split2(row < cnt && j < p.R ? s_z[row][j] * c : 0.f, hi, lo);
+            s_hi[row][j] = hi;
+            s_lo[row][j] = lo;
+        }
+        if (lane == 0) s_scale[row] = inv;
+    }
+    __syncthreads();
+    float acc[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < KB; ++k) {
+        const int j = k * 16 + tig * 4;
+        const uint2 h0 = *reinterpret_cast<const uint2 *>(&s_hi[g][j]), h1 = *reinterpret_cast<const uint2 *>(&s_hi[g + 8][j]);
+        const uint2 l0 = *reinterpret_cast<const uint2 *>(&s_lo[g][j]), l1 = *reinterpret_cast<const uint2 *>(&s_lo[g + 8][j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mma_t<TX>(acc[i], h0.x, h1.x, h0.y, h1.y, bv[i][k].x, bv[i][k].y);
+            mma_t<TX>(acc[i], l0.x, l1.x, l0.y, l1.y, bv[i][k].x, bv[i][k].y);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        if (rows[r] < 0) continue;
+        const float sc = s_scale[g + 8 * r];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int n = n0 + i * 8 + tig * 2 + e;
+                if (n < p.N)
+                    y[rows[r] * p.ldy + n] = from_f32<TY>(fmaf(acc[i][2 * r + e] * sc, scaling, yv[r][i][e]));
+            }
+    }
+}
+
+// ============================================================================ tiles
+// Ring of shared-memory stages between the load threads and the thread that issues the
+// MMAs.  Every load thread copies its share of a stage with cp.async and reports it kLag
+// stages later, when the copies have landed (one arrival per warp).
+template <int NS>
+struct Ring {
+    uint64_t full[NS], empty[NS], done;
+    __device__ void init(int warps)
+    {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&full[i], warps);
+            mbar_init(&empty[i], 1);
+        }
+        mbar_init(&done, 1);
+        fence_mbar_init();
+    }
+};
+
+// Load loop of one thread: issue(stage, i) starts the copies of step i.  Returns false if a
+// wait gave up.
+template <int NS, typename F>
+__device__ __forceinline__ bool ring_load(Ring<NS> &r, int steps, int *status, F &&issue)
+{
+    constexpr int kLag = NS - 1;
+    const int lane = threadIdx.x & 31;
+    bool ok = true;
+    for (int i = 0; i < steps + kLag; ++i) {
+        if (i < steps) {
+            if (i >= NS && ok) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            issue(i % NS, i);
+        }
+        cp_async_commit();
+        if (i >= kLag) {
+            cp_async_wait<kLag>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&r.full[(i - kLag) % NS]);
+        }
+    }
+    cp_async_wait<0>();
+    return ok;
+}
+
+// Issue loop of the MMA thread: mma(stage, i) issues the MMAs of step i.
+template <int NS, typename F>
+__device__ __forceinline__ void ring_mma(Ring<NS> &r, int steps, int *status, F &&mma)
+{
+    for (int i = 0; i < steps; ++i) {
+        if (!mbar_wait(&r.full[i % NS], (i / NS) & 1, status)) return;
+        tc_after();
+        mma(i % NS, i);
+        tc_commit(&r.empty[i % NS]);
+    }
+    tc_commit(&r.done);
+}
+
+__device__ __forceinline__ uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : 256u; }
+
+constexpr int kShrinkNS = 4;
+
+__host__ __device__ inline int shrink_w_bytes(bool grad, int R, int Kp)
+{
+    return grad ? (R > 64 ? 2 : 1) * 64 * 128 : Kp * 128;   // multiples of 1024
+}
+
+// z = X A^T of one tile of 128 tokens (kGrad: dz = s dY B), K split over the CTAs of a
+// cluster.  Operands: X [128 tokens][64 K] K-major; A [ranks][64 K] K-major, or B [64 n][ranks]
+// MN-major.  The partial sums meet in shared memory: each CTA adds 128 / S rows of all S
+// parts in rank order and writes them: z (fp32), z as pieces with the row's scale, and for
+// the weight gradients the adapters' largest magnitudes (fp16) or z_in's pieces (bf16).
+// Bound by the rows of X.
+template <typename TX, bool kGrad>
+__global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdParams p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ Ring<kShrinkNS> ring;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_tok[kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = cluster_size(), q = cluster_rank(), tile = blockIdx.x / S;
+    unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    pdl_wait();
+    pdl_trigger();
+    const int bin = __ldcg(p.tile_bin + tile);
+    if (bin < 0) return;   // (the whole cluster)
+    const int rank = rank_of(p, bin), R = p.R, Kp = p.Kp;
+    const int32_t *entry = p.entry_of + (size_t)tile * kTile;
+    if (rank == 0) {
+        if (p.z_out)
+            for (int i = q * (kWorkers + 32) + tid; i < kTile * R; i += S * (kWorkers + 32)) {
+                const int t = __ldcg(entry + i / R);
+                if (t >= 0) p.z_out[(size_t)t * R + i % R] = 0.f;
+            }
+        return;
+    }
+    if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);
+    if (tid == 0) ring.init(kWorkers / 32);
+    if (warp == kWorkers / 32) tc_alloc(&s_tmem, tmem_cols(Kp));
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem, sbuf = smem_u32(buf);
+    const int width = kGrad ? p.N : p.K;
+    const int blocks = (width + 63) / 64;
+    const int b_lo = (int)((long long)blocks * q / S), steps = (int)((long long)blocks * (q + 1) / S) - b_lo;
+    const int wb = shrink_w_bytes(kGrad, R, Kp), stage = kBlk + wb;
+    const int pitch = Kp + 4;   // floats of a row of the partial sums
+    if (warp < kWorkers / 32) {
+        const int c = tid & 7, r0 = tid >> 3;
+        const TX *X = static_cast<const TX *>(kGrad ? p.dy : p.x);
+        const long long ld = kGrad ? p.lddy : p.ldx;
+        const TX *W = kGrad ? static_cast<const TX *>(p.b) + (size_t)bin * p.N * R
+                            : static_cast<const TX *>(p.a) + (size_t)bin * R * p.K;
+        const TX *px[4];
+        bool live[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = s_tok[r0 + 32 * i];
+            live[i] = t >= 0;
+            px[i] = X + (live[i] ? t * ld : 0) + c * 8;
+        }
+        ring_load<kShrinkNS>(ring, steps, p.status, [&](int s, int i) {
+            const int k0 = (b_lo + i) * 64, k = k0 + c * 8;
+            const uint32_t xs = sbuf + s * stage, ws = xs + kBlk;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                cp_async16_or_zero(xs + swz(r0 + 32 * u, c), live[u] && k < width ? px[u] + k0 : X, live[u] && k < width);
+            if (kGrad) {
+                for (int u = 0; u < 2; ++u) {
+                    const int kk = r0 + 32 * u;
+                    for (int b = 0; b * 64 < R; ++b) {
+                        const bool in = k0 + kk < width && b * 64 + c * 8 < R;
+                        cp_async16_or_zero(ws + b * 8192 + swz(kk, c), in ? W + (size_t)(k0 + kk) * R + b * 64 + c * 8 : W, in);
+                    }
+                }
+            } else {
+                for (int j = r0; j < Kp; j += 32) {
+                    const bool in = k < width && j < R;
+                    cp_async16_or_zero(ws + swz(j, c), in ? W + (size_t)j * p.K + k : W, in);
+                }
+            }
+        });
+        mbar_wait(&ring.done, 0, p.status);
+        tc_after();
+        float *P = reinterpret_cast<float *>(buf);
+        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
+        for (int col = half * (Kp / 2); col < (half + 1) * (Kp / 2); col += 8) {
+            float v[8];
+            tc_ld8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
+            tc_wait_ld();
+            float4 *dst = reinterpret_cast<float4 *>(P + row * pitch + col);
+            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
+        tc_before();
+    } else if (lane == 0) {
+        const uint32_t idesc = idesc16<TX>(Kp, false, kGrad);
+        ring_mma<kShrinkNS>(ring, steps, p.status, [&](int s, int i) {
+            const uint32_t xs = sbuf + s * stage, ws = xs + kBlk;
+            const uint64_t da = sdesc_k(xs), db = kGrad ? sdesc_mn(ws, 8192) : sdesc_k(ws);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+                tc_mma16(tmem, da + 2 * kk, db + (kGrad ? 128 : 2) * kk, idesc, i > 0 || kk > 0);
+        });
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == kWorkers / 32) {
+        tc_after();
+        tc_dealloc(tmem, tmem_cols(Kp));
+    } else {
+        const int per = kTile / S;
+        const float scaling = kGrad ? __ldcg(p.scaling + bin) : 1.f;
+        const float apply_scale = kGrad ? 1.f : __ldcg(p.scaling + bin);
+        for (int r = q * per + warp; r < (q + 1) * per; r += kWorkers / 32) {
+            const int tok = s_tok[r];
+            const size_t pos = (size_t)tile * kTile + r;
+            float v[4], m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = lane + 32 * i;
+                v[i] = 0.f;
+                if (col < Kp) {
+                    const uint32_t at = sbuf + (uint32_t)(r * pitch + col) * 4;
+                    if (S > 1) {
+#pragma unroll 8
+                        for (int c = 0; c < S; ++c) v[i] += ld_cluster(peer_addr(at, c));
+                    } else {
+                        v[i] = reinterpret_cast<float *>(buf)[r * pitch + col];
+                    }
+                    if (col >= rank || tok < 0) v[i] = 0.f;   // (what lies past the rank is not used)
+                    v[i] *= scaling;
+                }
+                m = fmaxf(m, finite_or_0(v[i]));
+            }
+            m = warp_max(m);
+            float inv;
+            const float c = norm_scale(m, inv);
+            TX *limb = static_cast<TX *>(p.limb) + pos * 2 * Kp;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int col = lane + 32 * i;
+                if (col >= Kp) continue;
+                TX hi, lo;
+                split2(v[i] * (TcType<TX>::code ? 1.f : c), hi, lo);   // (bf16 has fp32's range)
+                limb[col] = hi;
+                limb[Kp + col] = lo;
+                if (p.z_out && tok >= 0 && col < R) p.z_out[(size_t)tok * R + col] = v[i];
+                if (kGrad && p.want_dw && !TcType<TX>::code && col < R) p.dz[pos * R + col] = v[i];
+            }
+            if (lane == 0) p.row_scale[pos] = (TcType<TX>::code ? 1.f : inv) * apply_scale;
+            if (kGrad && p.want_dw) {
+                float zm = 0.f;
+                TX *zl = static_cast<TX *>(p.zl) + pos * 2 * Kp;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int col = lane + 32 * i;
+                    const float z = col < rank && tok >= 0 ? __ldcg(p.z_in + (size_t)tok * R + col) : 0.f;
+                    if (TcType<TX>::code) {
+                        if (col < Kp) split2(z, zl[col], zl[Kp + col]);
+                    } else {
+                        zm = fmaxf(zm, finite_or_0(z));
+                    }
+                }
+                if (!TcType<TX>::code) {
+                    zm = warp_max(zm);
+                    if (lane == 0) {   // (a maximum of non-negative floats is one of their bits: any order)
+                        atomicMax(p.amax + bin, __float_as_uint(m));
+                        atomicMax(p.amax + p.n + bin, __float_as_uint(zm));
+                    }
                 }
             }
         }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], off);
-        if ((tid & 31) == 0) red[tid >> 5][i] = acc[i];
-    }
-    __syncthreads();
-    if (tid < 8) {
-        float v = 0.f;
-        for (int w = 0; w < kAdThreads / 32; ++w) v += red[w][tid];
-        if (kGrad && a >= 0) v *= p.scaling[a];
-        p.z[(size_t)t * p.R + j0 + tid] = j0 + tid < rank ? v : 0.f;
+    __syncwarp();
+    if (S > 1) cluster_sync();   // no CTA leaves while a peer reads its sums
+}
+
+// fp16 pools: dz and z as pieces under one scale per adapter (a sum over tokens has no
+// place for a scale per token), positions in order, a warp each.
+__global__ void __launch_bounds__(kWorkers) pieces_kernel(const AdParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const size_t pos = (size_t)blockIdx.x * (kWorkers / 32) + (threadIdx.x >> 5);
+    pdl_wait();
+    pdl_trigger();
+    const int bin = __ldcg(p.tile_bin + pos / kTile);
+    if (bin < 0) return;
+    const int rank = rank_of(p, bin);
+    if (rank == 0) return;
+    const int tok = __ldcg(p.entry_of + pos);
+    float inv;
+    const float cd = norm_scale(__uint_as_float(__ldcg(p.amax + bin)), inv);
+    const float cz = norm_scale(__uint_as_float(__ldcg(p.amax + p.n + bin)), inv);
+    __half *dl = static_cast<__half *>(p.dl) + pos * 2 * p.Kp, *zl = static_cast<__half *>(p.zl) + pos * 2 * p.Kp;
+    for (int col = lane; col < p.Kp; col += 32) {
+        const bool in = col < rank && tok >= 0;
+        split2(in ? __ldcg(p.dz + pos * p.R + col) * cd : 0.f, dl[col], dl[p.Kp + col]);
+        split2(in ? __ldcg(p.z_in + (size_t)tok * p.R + col) * cz : 0.f, zl[col], zl[p.Kp + col]);
     }
 }
 
-// y[t][n] = y_in[t][n] + s sum_j z[t][j] B[n][j] (kGrad: dx[t][k] = dx_in[t][k] + sum_j
-// dz[t][j] A[j][k]): one thread per element.
-template <typename TX, typename TY, bool kGrad>
-__global__ void __launch_bounds__(kAdThreads) expand_kernel(AdParams p)
+// da[a][j][k] = sum_t dz[t][j] x[t][k] and db[a][n][j] = s sum_t z[t][j] dy[t][n]: one product
+// D[c][j] = sum_t X[t][c] Z[t][j] over an adapter's tokens, 128 columns c of X per cluster,
+// its tokens dealt to the S CTAs 64 at a time.  Both operands are MN-major (rows are
+// tokens); Z's two pieces lie side by side as 2 Kp columns of one MMA.  The CTAs' parts meet
+// as in the shrink kernel.  Bound by reading X.
+constexpr int kGradNS = 4;
+__host__ __device__ inline int grad_z_bytes(int Kp) { return (2 * Kp + 63) / 64 * 8192; }
+
+template <typename TX>
+__global__ void __launch_bounds__(kWorkers + 32) grad_tile_kernel(const AdParams p)
 {
-    __shared__ float s_z[128];
-    const int t = blockIdx.x, tid = threadIdx.x, i = blockIdx.y * kAdThreads + tid;
-    pdl_trigger();
+    extern __shared__ unsigned char raw[];
+    __shared__ Ring<kGradNS> ring;
+    __shared__ uint32_t s_tmem;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int S = cluster_size(), q = cluster_rank();
+    const int tiles_a = (p.K + 127) / 128, ct = blockIdx.x / S;
+    const bool is_b = ct >= tiles_a;
+    const int c0 = (is_b ? ct - tiles_a : ct) * 128, width = is_b ? p.N : p.K, a = blockIdx.y;
+    unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
-    const int a = adapter_at(p, t);
-    const int rank = a < 0 ? 0 : rank_of(p, a);
-    if (tid < rank) s_z[tid] = p.zr[(size_t)t * p.R + tid];
-    __syncthreads();
-    const int width = kGrad ? p.K : p.N;
-    if (i >= width) return;
-    const TY *in = static_cast<const TY *>(p.y_in);
-    TY *y = static_cast<TY *>(p.y) + t * p.ldy + i;
-    if (in) in += t * p.ldy_in + i;
-    if (rank == 0) {
-        if (in != y) *y = in ? *in : from_f32<TY>(0.f);
+    pdl_trigger();
+    const int R = p.R, Kp = p.Kp, rank = rank_of(p, a);
+    const int cnt = rank ? __ldcg(p.counts + a) : 0;
+    float *out = is_b ? p.db + ((size_t)a * p.N + c0) * R : p.da + (size_t)a * R * p.K + c0;
+    const int cols = min(128, width - c0);
+    if (cnt == 0) {   // (the whole cluster)
+        if (p.accumulate) return;
+        if (is_b) {
+            for (int i = q * (kWorkers + 32) + tid; i < cols * R; i += S * (kWorkers + 32)) out[i] = 0.f;
+        } else {
+            for (int i = q * (kWorkers + 32) + tid; i < 128 * R; i += S * (kWorkers + 32))
+                if ((i & 127) < cols) out[(size_t)(i >> 7) * p.K + (i & 127)] = 0.f;
+        }
         return;
     }
-    float acc = 0.f;
-    if (kGrad) {
-        const TX *A = static_cast<const TX *>(p.a) + (size_t)a * p.R * p.K + i;
-        for (int j = 0; j < rank; ++j) acc = fmaf(s_z[j], f32_of(A[(size_t)j * p.K]), acc);
-    } else {
-        const TX *B = static_cast<const TX *>(p.b) + ((size_t)a * p.N + i) * p.R;
-        for (int j = 0; j < rank; ++j) acc = fmaf(s_z[j], f32_of(B[j]), acc);
-        acc *= p.scaling[a];
-    }
-    *y = from_f32<TY>((in ? f32_of(*in) : 0.f) + acc);
-}
-
-// da[a][j][k] = sum_t dz[t][j] x[t][k] (kB: db[a][n][j] = s sum_t z[t][j] dy[t][n]): one CTA per
-// adapter, rank and 128 columns, over the batch's tokens in order.
-template <typename TX, bool kB>
-__global__ void __launch_bounds__(kAdThreads) grad_kernel(AdParams p)
-{
-    const int c = blockIdx.x * kAdThreads + threadIdx.x, j = blockIdx.y, a = blockIdx.z;
-    pdl_trigger();
-    pdl_wait();
-    const int width = kB ? p.N : p.K;
-    if (c >= width) return;
-    const int rank = rank_of(p, a);
-    const TX *x = static_cast<const TX *>(kB ? p.dy : p.x);
-    const long long ld = kB ? p.lddy : p.ldx;
-    float acc = 0.f;
-    bool any = false;
-    if (j < rank)
-        for (int t = 0; t < p.T; ++t) {
-            if (p.adapter_of[t] != a) continue;
-            any = true;
-            acc = fmaf(p.zr[(size_t)t * p.R + j], f32_of(x[t * ld + c]), acc);
+    const size_t pos0 = (size_t)__ldcg(p.seg + a);
+    if (tid == 0) ring.init(kWorkers / 32);
+    if (warp == kWorkers / 32) tc_alloc(&s_tmem, tmem_cols(2 * Kp));
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem, sbuf = smem_u32(buf);
+    const int blocks = (cnt + 63) / 64, steps = (blocks - q + S - 1) / S;   // token blocks q, q + S, ..
+    const int stage = 2 * 8192 + grad_z_bytes(Kp);
+    const int pitch = is_b ? Kp + 4 : 128 + 4;
+    float *P = reinterpret_cast<float *>(buf);
+    if (warp < kWorkers / 32) {
+        const TX *X = static_cast<const TX *>(is_b ? p.dy : p.x);
+        const long long ld = is_b ? p.lddy : p.ldx;
+        const TX *Z = static_cast<const TX *>(is_b ? p.zl : p.dl);
+        const int cx = tid & 15, rx = tid >> 4, ch = Kp / 4;   // 16-byte chunks of a row of Z
+        ring_load<kGradNS>(ring, steps, p.status, [&](int s, int i) {
+            const size_t pos = pos0 + (size_t)(q + i * S) * 64;
+            const uint32_t xs = sbuf + s * stage, zs = xs + 2 * 8192;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int row = rx + 16 * u, t = __ldcg(p.entry_of + pos + row);
+                const bool in = t >= 0 && cx * 8 < cols;
+                cp_async16_or_zero(xs + (cx >> 3) * 8192 + swz(row, cx & 7), in ? X + t * ld + c0 + cx * 8 : X, in);
+            }
+            for (int e = tid; e < 64 * ch; e += kWorkers) {
+                const int row = e / ch, c = e % ch;
+                cp_async16_or_zero(zs + (c >> 3) * 8192 + swz(row, c & 7), Z + (pos + row) * 2 * Kp + c * 8, true);
+            }
+        });
+        if (steps > 0) mbar_wait(&ring.done, 0, p.status);
+        tc_after();
+        const int c = (warp & 3) * 32 + lane, half = warp >> 2;
+        for (int j = half * (Kp / 2); j < (half + 1) * (Kp / 2); j += 8) {
+            float v[8] = {}, w[8] = {};
+            if (steps > 0) {
+                const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + j;
+                tc_ld8(t, v);
+                tc_ld8(t + Kp, w);
+                tc_wait_ld();
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (is_b) P[c * pitch + j + e] = v[e] + w[e];
+                else P[(j + e) * pitch + c] = v[e] + w[e];
+            }
         }
-    if (kB) acc *= p.scaling[a];
-    float *out = p.out + (kB ? ((size_t)a * p.N + c) * p.R + j : ((size_t)a * p.R + j) * p.K + c);
-    if (!p.accumulate) *out = any ? acc : 0.f;
-    else if (any) *out += acc;
+        tc_before();
+    } else if (lane == 0 && steps > 0) {
+        const uint32_t idesc = idesc16<TX>(2 * Kp, true, true);
+        ring_mma<kGradNS>(ring, steps, p.status, [&](int s, int i) {
+            const uint32_t xs = sbuf + s * stage;
+            const uint64_t da = sdesc_mn(xs, 8192), db = sdesc_mn(xs + 2 * 8192, 8192);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) tc_mma16(tmem, da + 128 * kk, db + 128 * kk, idesc, i > 0 || kk > 0);
+        });
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == kWorkers / 32) {
+        tc_after();
+        tc_dealloc(tmem, tmem_cols(2 * Kp));
+    } else {
+        float scale = is_b ? __ldcg(p.scaling + a) : 1.f, inv = 1.f;
+        if (!TcType<TX>::code) {
+            norm_scale(__uint_as_float(__ldcg(p.amax + (is_b ? p.n : 0) + a)), inv);
+            scale *= inv;
+        }
+        const int per = is_b ? R / 4 : 32;                    // float4 per row of the output
+        const int rows = is_b ? cols : R;
+        for (int i = q * kWorkers + tid; i < rows * per; i += S * kWorkers) {
+            const int row = i / per, c4 = (i % per) * 4;
+            if (!is_b && c4 >= cols) continue;                // (K is a multiple of 8)
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            const uint32_t at = sbuf + (uint32_t)(row * pitch + c4) * 4;
+#pragma unroll 8
+            for (int c = 0; c < S; ++c) {
+                const float4 o = S > 1 ? ld_cluster4(peer_addr(at, c)) : *reinterpret_cast<float4 *>(P + row * pitch + c4);
+                v.x += o.x;
+                v.y += o.y;
+                v.z += o.z;
+                v.w += o.w;
+            }
+            float *f = &v.x;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = (is_b ? c4 + e : row) < rank ? f[e] * scale : 0.f;
+            float4 *dst = reinterpret_cast<float4 *>(is_b ? out + (size_t)row * R + c4 : out + (size_t)row * p.K + c4);
+            if (p.accumulate) {
+                float4 o = *dst;
+                float *g = &o.x;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if ((is_b ? c4 + e : row) < rank) g[e] += f[e];
+                v = o;
+            }
+            *dst = v;
+        }
+    }
+    __syncwarp();
+    if (S > 1) cluster_sync();
 }
 
+// y[t][n] = y_in[t][n] + sum_j z[t][j] B[n][j] (kGrad: dx = dx_in + dz A) of one tile of 128
+// tokens and a run of 128-column blocks.  Operands: z's pieces [128 tokens][2 Kp] K-major,
+// loaded once; B [128 n][ranks] K-major, or A [ranks][128 k] MN-major, two stages; D double
+// buffered in TMEM.  Eight epilogue warps (32 rows x 64 columns each) turn D's rows into
+// coalesced rows through shared memory and add y_in, loaded ahead of the product.  Bound by
+// reading y_in and writing y.
+constexpr int kExpandThreads = kWorkers + 32 + 64;   // epilogue, MMA, load warps
+constexpr int kScratch = 32 * 36 * 4;                // a warp's 32 x 32 block, padded rows
+
+__host__ __device__ inline int expand_z_bytes(int Kp) { return (2 * Kp + 63) / 64 * kBlk; }
+__host__ __device__ inline int expand_w_bytes(bool grad, int Kp) { return grad ? Kp * 256 : (Kp + 63) / 64 * kBlk; }
+
+template <typename TX, typename TY, bool kGrad, bool kVec>
+__global__ void __launch_bounds__(kExpandThreads, 1) expand_tile_kernel(const AdParams p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t wfull[2], wempty[2], tfull[2], tempty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_tok[kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tile = blockIdx.x;
+    unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    pdl_wait();
+    pdl_trigger();
+    const int bin = __ldcg(p.tile_bin + tile);
+    if (bin < 0) return;
+    const int rank = rank_of(p, bin), R = p.R, Kp = p.Kp, width = kGrad ? p.K : p.N;
+    const int nt_all = (width + 127) / 128;
+    const int nt0 = (int)((long long)nt_all * blockIdx.y / gridDim.y);
+    const int nts = (int)((long long)nt_all * (blockIdx.y + 1) / gridDim.y) - nt0;
+    const TY *in = static_cast<const TY *>(p.y_in);
+    TY *y = static_cast<TY *>(p.y);
+    if (tid < kTile) s_tok[tid] = __ldcg(p.entry_of + (size_t)tile * kTile + tid);
+    if (rank == 0) {
+        if (in == y) return;   // in place: nothing to add
+        __syncthreads();
+        const int lo = nt0 * 128, hi = min((nt0 + nts) * 128, width);
+        for (int r = warp; r < kTile; r += kExpandThreads / 32) {
+            const int t = s_tok[r];
+            if (t < 0) continue;
+            for (int c = lo + lane; c < hi; c += 32) y[t * p.ldy + c] = in ? in[t * p.ldy_in + c] : from_f32<TY>(0.f);
+        }
+        return;
+    }
+    const uint32_t zs = smem_u32(buf), ws = zs + expand_z_bytes(Kp), wb = expand_w_bytes(kGrad, Kp);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&wfull[i], 2);
+            mbar_init(&wempty[i], 1);
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kWorkers / 32);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kWorkers / 32) tc_alloc(&s_tmem, 256);
+    if (warp < kWorkers / 32) {   // z's pieces: chunk i of a row is columns 8 i ..
+        const TX *Z = static_cast<const TX *>(p.limb) + (size_t)tile * kTile * 2 * Kp;
+        const int ch = Kp / 4;
+        for (int e = tid; e < kTile * ch; e += kWorkers) {
+            const int row = e / ch, c = e % ch;
+            cp_async16_or_zero(zs + (c >> 3) * kBlk + swz(row, c & 7), Z + (size_t)row * 2 * Kp + c * 8, true);
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_async_smem();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = s_tmem;
+    if (warp > kWorkers / 32) {   // ---- weights
+        const int lt = tid - (kWorkers + 32);
+        const TX *W = kGrad ? static_cast<const TX *>(p.a) + (size_t)bin * R * p.K
+                            : static_cast<const TX *>(p.b) + (size_t)bin * p.N * R;
+        const int ch = Kp / 8;
+        bool ok = true;
+        for (int i = 0; i < nts && ok; ++i) {
+            const int s = i & 1, n0 = (nt0 + i) * 128;
+            const uint32_t w = ws + s * wb;
+            if (i >= 2) ok = mbar_wait(&wempty[s], ((i >> 1) & 1) ^ 1, p.status);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            if (kGrad) {   // rows past the rank become zeros: they meet z's zeros in the product
+                for (int e = lt; e < Kp * 16; e += 64) {
+                    const int j = e >> 4, c = e & 15;
+                    const bool v = j < rank && n0 + c * 8 < width;
+                    cp_async16_or_zero(w + (c >> 3) * (Kp * 128) + swz(j, c & 7), v ? W + (size_t)j * p.K + n0 + c * 8 : W, v);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+            } else {
+                for (int e = lt; e < 128 * ch; e += 64) {
+                    const int n = e / ch, c = e % ch;
+                    const bool v = c * 8 < rank && n0 + n < width;
+                    cp_async16_or_zero(w + (c >> 3) * kBlk + swz(n, c & 7), v ? W + (size_t)(n0 + n) * R + c * 8 : W, v);
+                }
+                cp_async_commit();
+                cp_async_wait<0>();
+                if (rank & 7)   // columns past the rank inside a chunk
+                    for (int e = lt; e < 128 * ch; e += 64) {
+                        const int n = e / ch, c = e % ch;
+                        if (c != rank >> 3) continue;
+                        TX *v = reinterpret_cast<TX *>(buf + (w - zs) + (c >> 3) * kBlk + swz(n, c & 7));
+                        for (int j = rank & 7; j < 8; ++j) v[j] = from_f32<TX>(0.f);
+                    }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&wfull[s]);
+        }
+    } else if (warp == kWorkers / 32) {   // ---- products
+        if (lane == 0) {
+            const uint32_t idesc = idesc16<TX>(128, false, kGrad);
+            for (int i = 0; i < nts; ++i) {
+                const int s = i & 1;
+                if (!mbar_wait(&wfull[s], (i >> 1) & 1, p.status)) break;
+                if (i >= 2 && !mbar_wait(&tempty[s], ((i >> 1) & 1) ^ 1, p.status)) break;
+                tc_after();
+                const uint32_t w = ws + s * wb;
+                for (int l = 0; l < 2; ++l)
+                    for (int j = 0; j < Kp; j += 16) {
+                        const int at = l * Kp + j;
+                        const uint64_t da = sdesc_k(zs + (at >> 6) * kBlk) + ((at & 63) >> 3);
+                        const uint64_t db = kGrad ? sdesc_mn(w, Kp * 128) + 8 * j : sdesc_k(w + (j >> 6) * kBlk) + ((j & 63) >> 3);
+                        tc_mma16(tmem + s * 128, da, db, idesc, at > 0);
+                    }
+                tc_commit(&wempty[s]);
+                tc_commit(&tfull[s]);
+            }
+        }
+    } else {   // ---- epilogue
+        const int q4 = warp & 3, half = warp >> 2;
+        float *sc = reinterpret_cast<float *>(buf + expand_z_bytes(Kp) + 2 * wb + warp * kScratch);
+        const float scale = __ldcg(p.row_scale + (size_t)tile * kTile + q4 * 32 + lane);
+        constexpr int VE = kVec ? 16 / sizeof(TY) : 1;   // elements of a lane's access
+        constexpr int LPR = 32 / VE;                     // lanes of a row
+        constexpr int NI = LPR;                          // accesses of a 32 x 32 block
+        constexpr int RPI = 32 / LPR;                    // rows of an access
+        const int col = (lane % LPR) * VE, rl = lane / LPR;
+        const int passes = 2 * nts;
+        using V = uint4;
+        V pre[kVec ? NI : 1];
+        auto fetch = [&](int ps) {
+            if (!kVec || !in) return;
+            const int n = (nt0 + (ps >> 1)) * 128 + half * 64 + (ps & 1) * 32 + col;
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int t = s_tok[q4 * 32 + i * RPI + rl];
+                if (t >= 0 && n < width) pre[kVec ? i : 0] = *reinterpret_cast<const V *>(in + t * p.ldy_in + n);
+            }
+        };
+        fetch(0);
+        bool ok = true;
+        for (int ps = 0; ps < passes; ++ps) {
+            const int i = ps >> 1, s = i & 1;
+            if (!(ps & 1)) {
+                ok = mbar_wait(&tfull[s], (i >> 1) & 1, p.status);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                tc_after();
+            }
+            const uint32_t t0 = tmem + ((uint32_t)(q4 * 32) << 16) + s * 128 + half * 64 + (ps & 1) * 32;
+            float v[4][8];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tc_ld8(t0 + 8 * c, v[c]);
+            tc_wait_ld();
+            if (ps & 1) {
+                tc_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[s]);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[c][e] *= scale;
+                *reinterpret_cast<float4 *>(sc + lane * 36 + 8 * c) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
+                *reinterpret_cast<float4 *>(sc + lane * 36 + 8 * c + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
+            }
+            __syncwarp();
+            const int n = (nt0 + i) * 128 + half * 64 + (ps & 1) * 32 + col;
+            if (kVec) {
+                V o[NI];
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    float f[8];
+                    const float *d = sc + (k * RPI + rl) * 36 + col;
+                    *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(d);
+                    if (VE == 8) *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(d + 4);
+                    TY *w = reinterpret_cast<TY *>(&o[k]);
+                    const TY *b = reinterpret_cast<const TY *>(&pre[kVec ? k : 0]);
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) w[e] = from_f32<TY>((in ? f32_of(b[e]) : 0.f) + f[e]);
+                }
+                if (ps + 1 < passes) fetch(ps + 1);
+#pragma unroll
+                for (int k = 0; k < NI; ++k) {
+                    const int t = s_tok[q4 * 32 + k * RPI + rl];
+                    if (t >= 0 && n < width) *reinterpret_cast<V *>(y + t * p.ldy + n) = o[k];
+                }
+            } else {
+                for (int r = 0; r < 32; ++r) {
+                    const int t = s_tok[q4 * 32 + r];
+                    if (t >= 0 && n < width)
+                        y[t * p.ldy + n] = from_f32<TY>((in ? f32_of(in[t * p.ldy_in + n]) : 0.f) + sc[r * 36 + lane]);
+                }
+            }
+            __syncwarp();
+        }
+        tc_before();
+    }
+    __syncthreads();
+    if (warp == kWorkers / 32) {
+        tc_after();
+        tc_dealloc(tmem, 256);
+    }
+}
+
+// ============================================================================ host
 size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 size_t dtype_bytes(int dtype) { return dtype == MOE_DTYPE_F32 ? 4 : 2; }
 bool known_dtype(int dtype) { return dtype >= MOE_DTYPE_F16 && dtype <= MOE_DTYPE_F32; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
+int tiles_max(const moe_adapters_desc &d, int T) { return (T + kTile - 1) / kTile + std::min(d.n_adapters + 1, T); }
+int few_splits(const moe_adapters_desc &d) { return (d.in_features + kFewK - 1) / kFewK; }
+int rank_pad(const moe_adapters_desc &d) { return (d.max_rank + 15) / 16 * 16; }
+
+// a call's workspace: the small path's partial sums share the bytes of the other path
 struct AdWs {
-    size_t z, total;
+    size_t seg, counts, entry_of, tile_bin, hist, limb, row_scale, zl, dl, dz, amax, total;
 };
 
 AdWs ad_layout(const moe_adapters_desc &d, int T)
 {
     AdWs w;
+    const size_t bins = d.n_adapters + 1, tiles = tiles_max(d, T), rows = tiles * kTile;
+    const size_t pieces = rows * 2 * rank_pad(d) * 2;
     size_t o = 0;
-    w.z = o; o = up256(o + (size_t)T * d.max_rank * 4);
-    w.total = std::max<size_t>(o, 256);
+    w.seg = o; o = up256(o + (bins + 1) * 4);
+    w.counts = o; o = up256(o + bins * 4);
+    w.entry_of = o; o = up256(o + rows * 4);
+    w.tile_bin = o; o = up256(o + tiles * 4);
+    w.hist = o; o = up256(o + ((size_t)T + kSortChunk - 1) / kSortChunk * bins * 4);
+    w.limb = o; o = up256(o + pieces);
+    w.row_scale = o; o = up256(o + rows * 4);
+    w.zl = o; o = up256(o + pieces);
+    w.dl = o; o = up256(o + pieces);
+    w.dz = o; o = up256(o + rows * d.max_rank * 4);
+    w.amax = o; o = up256(o + 2 * bins * 4);
+    const size_t few = (size_t)few_splits(d) * std::min(T, kFewT) * d.max_rank * 4;
+    w.total = std::max(o, up256(few));
     return w;
 }
 
@@ -190,7 +1002,7 @@ bool ld_ok(int64_t ld, int width) { return ld >= width && (uint64_t)ld < (1ull <
 // rows of 16-bit elements that 16-byte loads can read
 bool rows16_ok(const void *p, int64_t ld, int width) { return p && aligned16(p) && ld_ok(ld, width) && ld % 8 == 0; }
 
-// rows that the kernels read and write element by element or wider as they are aligned
+// rows that are read and written element by element, or wider as they are aligned
 bool out_ok(const void *p, int dtype, int64_t ld, int width)
 {
     return p && known_dtype(dtype) && ld_ok(ld, width) && reinterpret_cast<uintptr_t>(p) % dtype_bytes(dtype) == 0;
@@ -209,8 +1021,11 @@ int check_ws(const moe_adapters *h, int T, const void *ws, size_t bytes)
     return MOE_OK;
 }
 
-AdParams ad_params(const moe_adapters *h, const int32_t *adapter_of, int T)
+AdParams ad_params(const moe_adapters *h, const int32_t *adapter_of, int T, void *ws)
 {
+    const moe_adapters_desc &d = h->desc;
+    const AdWs w = ad_layout(d, T);
+    auto at = [&](size_t off) { return static_cast<char *>(ws) + off; };
     AdParams p = {};
     p.a = h->w.a;
     p.b = h->w.b;
@@ -218,46 +1033,171 @@ AdParams ad_params(const moe_adapters *h, const int32_t *adapter_of, int T)
     p.rank = h->w.rank;
     p.adapter_of = adapter_of;
     p.T = T;
-    p.K = h->desc.in_features;
-    p.N = h->desc.out_features;
-    p.R = h->desc.max_rank;
-    p.n = h->desc.n_adapters;
+    p.K = d.in_features;
+    p.N = d.out_features;
+    p.R = d.max_rank;
+    p.Kp = rank_pad(d);
+    p.n = d.n_adapters;
     p.status = h->d_status;
+    p.seg = reinterpret_cast<int32_t *>(at(w.seg));
+    p.counts = reinterpret_cast<int32_t *>(at(w.counts));
+    p.entry_of = reinterpret_cast<int32_t *>(at(w.entry_of));
+    p.tile_bin = reinterpret_cast<int32_t *>(at(w.tile_bin));
+    p.limb = at(w.limb);
+    p.row_scale = reinterpret_cast<float *>(at(w.row_scale));
+    p.zl = at(w.zl);
+    p.dl = d.dtype == MOE_DTYPE_F16 ? at(w.dl) : at(w.limb);   // bf16: dz's pieces serve both products
+    p.dz = reinterpret_cast<float *>(at(w.dz));
+    p.amax = reinterpret_cast<unsigned *>(at(w.amax));
+    p.z_part = reinterpret_cast<float *>(ws);
+    p.splits = few_splits(d);
     return p;
 }
 
-template <typename TX, bool kGrad>
-cudaError_t run_expand(const AdParams &p, int y_dtype, cudaStream_t s)
+cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStream_t s)
 {
-    const dim3 grid(p.T, ((kGrad ? p.K : p.N) + kAdThreads - 1) / kAdThreads);
+    SortParams q = {};
+    q.key = p.adapter_of;
+    q.n = p.T;
+    q.E = p.n + 1;
+    q.align = kTile;
+    q.none_bin = p.n;
+    q.counts = p.counts;
+    q.seg = p.seg;
+    q.entry_of = p.entry_of;
+    q.tile_bin = p.tile_bin;
+    q.max_tiles = tiles_max(h->desc, p.T);
+    q.zero = p.amax;
+    q.n_zero = 2 * p.n;
+    q.hist = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + ad_layout(h->desc, p.T).hist);
+    q.status = p.status;
+    return launch_sort(q, s);
+}
+
+template <typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                           const AdParams &p)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// CTAs of a cluster that share `blocks` steps of work so that `units` clusters give every SM
+// about two CTAs
+int split_of(long long units, int blocks, int num_sms)
+{
+    int S = 1;
+    while (S < kMaxSplit && units * S < 2 * num_sms && 2 * S <= blocks) S *= 2;
+    return S;
+}
+
+template <typename TX, bool kGrad>
+cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
+{
+    const int tiles = tiles_max(h->desc, p.T);
+    const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, h->num_sms);
+    const size_t ring = (size_t)kShrinkNS * (kBlk + shrink_w_bytes(kGrad, p.R, p.Kp));
+    const size_t sums = (size_t)kTile * (p.Kp + 4) * 4;
+    return launch_cluster(shrink_tile_kernel<TX, kGrad>, dim3(tiles * S), kWorkers + 32, 1024 + std::max(ring, sums), S,
+                          s, p);
+}
+
+template <typename TX>
+cudaError_t run_grad(const moe_adapters *h, const AdParams &p, cudaStream_t s)
+{
+    const int tiles = (p.K + 127) / 128 + (p.N + 127) / 128, live = std::max(1, std::min(p.n, p.T));
+    const int S = split_of((long long)tiles * live, (p.T / live + 63) / 64, h->num_sms);
+    const size_t ring = (size_t)kGradNS * (2 * 8192 + grad_z_bytes(p.Kp));
+    const size_t sums = (size_t)std::max(128 * (p.Kp + 4), p.Kp * 132) * 4;
+    return launch_cluster(grad_tile_kernel<TX>, dim3(tiles * S, p.n), kWorkers + 32, 1024 + std::max(ring, sums), S, s,
+                          p);
+}
+
+template <typename TX, typename TY, bool kGrad>
+cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStream_t s)
+{
+    const int tiles = tiles_max(h->desc, p.T), width = kGrad ? p.K : p.N, nts = (width + 127) / 128;
+    const int groups = std::max(1, std::min(nts, 2 * h->num_sms / tiles));
+    const size_t smem = 1024 + expand_z_bytes(p.Kp) + 2 * (size_t)expand_w_bytes(kGrad, p.Kp) + kWorkers / 32 * kScratch;
+    const int es = (int)sizeof(TY);
+    auto wide = [&](const void *q, long long ld) { return !q || (aligned16(q) && ld * es % 16 == 0); };
+    const bool vec = width * es % 16 == 0 && wide(p.y, p.ldy) && wide(p.y_in, p.ldy_in);
+    return launch_cluster(vec ? expand_tile_kernel<TX, TY, kGrad, true> : expand_tile_kernel<TX, TY, kGrad, false>,
+                          dim3(tiles, groups), kExpandThreads, smem, 1, s, p);
+}
+
+template <typename TX, bool kGrad>
+cudaError_t run_expand(const moe_adapters *h, const AdParams &p, int y_dtype, cudaStream_t s)
+{
     switch (y_dtype) {
-    case MOE_DTYPE_F16: return launch_chained(expand_kernel<TX, __half, kGrad>, grid, kAdThreads, 0, s, p);
-    case MOE_DTYPE_BF16: return launch_chained(expand_kernel<TX, __nv_bfloat16, kGrad>, grid, kAdThreads, 0, s, p);
-    default: return launch_chained(expand_kernel<TX, float, kGrad>, grid, kAdThreads, 0, s, p);
+    case MOE_DTYPE_F16: return run_expand_tiles<TX, __half, kGrad>(h, p, s);
+    case MOE_DTYPE_BF16: return run_expand_tiles<TX, __nv_bfloat16, kGrad>(h, p, s);
+    default: return run_expand_tiles<TX, float, kGrad>(h, p, s);
+    }
+}
+
+template <typename TX, typename TY>
+cudaError_t run_few_expand(const AdParams &p, cudaStream_t s)
+{
+    const dim3 grid((p.N + kFewN - 1) / kFewN, p.T);
+    const int kb = p.Kp / 16;
+    if (kb <= 1) return launch_chained(expand_few_kernel<TX, TY, 1>, grid, kFewThreads, 0, s, p);
+    if (kb <= 2) return launch_chained(expand_few_kernel<TX, TY, 2>, grid, kFewThreads, 0, s, p);
+    if (kb <= 4) return launch_chained(expand_few_kernel<TX, TY, 4>, grid, kFewThreads, 0, s, p);
+    return launch_chained(expand_few_kernel<TX, TY, 8>, grid, kFewThreads, 0, s, p);
+}
+
+template <typename TX>
+cudaError_t run_few(const AdParams &p, int y_dtype, cudaStream_t s)
+{
+    const dim3 grid(p.splits, p.T);
+    const int nb = p.R / 8;
+    const cudaError_t e = nb <= 1   ? launch_chained(shrink_few_kernel<TX, 1>, grid, kFewThreads, 0, s, p)
+                          : nb <= 2 ? launch_chained(shrink_few_kernel<TX, 2>, grid, kFewThreads, 0, s, p)
+                          : nb <= 4 ? launch_chained(shrink_few_kernel<TX, 4>, grid, kFewThreads, 0, s, p)
+                          : nb <= 8 ? launch_chained(shrink_few_kernel<TX, 8>, grid, kFewThreads, 0, s, p)
+                                    : launch_chained(shrink_few_kernel<TX, 16>, grid, kFewThreads, 0, s, p);
+    if (e != cudaSuccess) return e;
+    switch (y_dtype) {
+    case MOE_DTYPE_F16: return run_few_expand<TX, __half>(p, s);
+    case MOE_DTYPE_BF16: return run_few_expand<TX, __nv_bfloat16>(p, s);
+    default: return run_few_expand<TX, float>(p, s);
     }
 }
 
 template <typename TX>
-cudaError_t run_apply(const AdParams &p, int y_dtype, cudaStream_t s)
+cudaError_t run_apply(const moe_adapters *h, const AdParams &p, int y_dtype, void *ws, cudaStream_t s)
 {
-    const cudaError_t e = launch_chained(shrink_kernel<TX, false>, dim3(p.T, p.R / 8), kAdThreads, 0, s, p);
-    return e != cudaSuccess ? e : run_expand<TX, false>(p, y_dtype, s);
+    if (p.T <= kFewT) return run_few<TX>(p, y_dtype, s);
+    cudaError_t e = run_sort(h, p, ws, s);
+    if (e == cudaSuccess) e = run_shrink<TX, false>(h, p, s);
+    return e != cudaSuccess ? e : run_expand<TX, false>(h, p, y_dtype, s);
 }
 
 template <typename TX>
-cudaError_t run_backward(AdParams p, const float *z, int dx_dtype, float *da, float *db, cudaStream_t s)
+cudaError_t run_backward(const moe_adapters *h, const AdParams &p, int dx_dtype, void *ws, cudaStream_t s)
 {
-    cudaError_t e = cudaSuccess;
-    if (p.T) e = launch_chained(shrink_kernel<TX, true>, dim3(p.T, p.R / 8), kAdThreads, 0, s, p);
-    if (e == cudaSuccess && p.T && p.y) e = run_expand<TX, true>(p, dx_dtype, s);
-    if (e != cudaSuccess || !da) return e;
-    p.out = da;
-    e = launch_chained(grad_kernel<TX, false>, dim3((p.K + kAdThreads - 1) / kAdThreads, p.R, p.n), kAdThreads, 0, s, p);
-    if (e != cudaSuccess) return e;
-    p.out = db;
-    p.zr = z;
-    return launch_chained(grad_kernel<TX, true>, dim3((p.N + kAdThreads - 1) / kAdThreads, p.R, p.n), kAdThreads, 0, s,
-                          p);
+    cudaError_t e = run_sort(h, p, ws, s);
+    if (e == cudaSuccess && p.T) e = run_shrink<TX, true>(h, p, s);
+    if (e == cudaSuccess && p.want_dw && p.T && !TcType<TX>::code)
+        e = launch_chained(pieces_kernel, dim3(tiles_max(h->desc, p.T) * (kTile / (kWorkers / 32))), kWorkers, 0, s, p);
+    if (e == cudaSuccess && p.want_dw) e = run_grad<TX>(h, p, s);
+    return e != cudaSuccess || !p.y ? e : run_expand<TX, true>(h, p, dx_dtype, s);
 }
 
 }  // namespace
@@ -328,18 +1268,17 @@ int moe_adapters_apply(const moe_adapters *h, const void *x, int64_t ldx, const 
         return MOE_ERR_INVALID_ARG;
     const int rc = check_ws(h, T, ws, ws_bytes);
     if (rc) return rc;
-    AdParams p = ad_params(h, adapter_of, T);
+    AdParams p = ad_params(h, adapter_of, T, ws);
     p.x = x;
     p.ldx = ldx;
     p.y_in = y_in;
     p.ldy_in = ldy_in;
     p.y = y;
     p.ldy = ldy;
-    p.z = z ? z : reinterpret_cast<float *>(static_cast<char *>(ws) + ad_layout(d, T).z);
-    p.zr = p.z;
+    p.z_out = z;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return cuda_status(d.dtype == MOE_DTYPE_F16 ? run_apply<__half>(p, y_dtype, s)
-                                                : run_apply<__nv_bfloat16>(p, y_dtype, s));
+    return cuda_status(d.dtype == MOE_DTYPE_F16 ? run_apply<__half>(h, p, y_dtype, ws, s)
+                                                : run_apply<__nv_bfloat16>(h, p, y_dtype, ws, s));
 }
 
 int moe_adapters_backward(const moe_adapters *h, const void *x, int64_t ldx, const float *z, const void *dy,
@@ -361,9 +1300,10 @@ int moe_adapters_backward(const moe_adapters *h, const void *x, int64_t ldx, con
     if ((T == 0 && (!da || accumulate)) || (!dx && !da)) return MOE_OK;
     const int rc = check_ws(h, T, ws, ws_bytes);
     if (rc) return rc;
-    AdParams p = ad_params(h, adapter_of, T);
+    AdParams p = ad_params(h, adapter_of, T, ws);
     p.x = x;
     p.ldx = ldx;
+    p.z_in = z;
     p.dy = dy;
     p.lddy = lddy;
     p.y_in = dx_in;
@@ -371,11 +1311,12 @@ int moe_adapters_backward(const moe_adapters *h, const void *x, int64_t ldx, con
     p.y = dx;
     p.ldy = lddx;
     p.accumulate = accumulate != 0;
-    p.z = reinterpret_cast<float *>(static_cast<char *>(ws) + ad_layout(d, T).z);
-    p.zr = p.z;
+    p.want_dw = da != nullptr;
+    p.da = da;
+    p.db = db;
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return cuda_status(d.dtype == MOE_DTYPE_F16 ? run_backward<__half>(p, z, dx_dtype, da, db, s)
-                                                : run_backward<__nv_bfloat16>(p, z, dx_dtype, da, db, s));
+    return cuda_status(d.dtype == MOE_DTYPE_F16 ? run_backward<__half>(h, p, dx_dtype, ws, s)
+                                                : run_backward<__nv_bfloat16>(h, p, dx_dtype, ws, s));
 }
 
 int moe_adapters_get_device_status(const moe_adapters *h, int *status)

@@ -113,6 +113,10 @@ struct SortParams {
     int32_t *seg;         // [E + 1] first position of each group
     int32_t *row_of;      // optional [n] position of each entry
     int32_t *entry_of;    // optional: entry at each position, -1 in the padding of a group
+    int32_t *tile_bin;    // optional [max_tiles]: bin of each `align` positions, -1 behind the last
+    int max_tiles;
+    unsigned *zero;       // optional: n_zero words to clear
+    int n_zero;
     int32_t *hist;        // scratch [ceil(n / kSortChunk)][E] (unused when n <= kSortChunk)
     int *status;
 };

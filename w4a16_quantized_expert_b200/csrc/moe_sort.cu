@@ -143,6 +143,14 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
         if (p.row_of) p.row_of[i] = pos;
         if (p.entry_of && pos >= 0) p.entry_of[pos] = i;
     }
+    if (chunk == 0) {
+        for (int i = tid; i < p.n_zero; i += kSortThreads) p.zero[i] = 0u;
+        if (p.tile_bin) {
+            for (int e = tid; e < p.E; e += kSortThreads)
+                for (int i = seg[e] / p.align; i < seg[e + 1] / p.align; ++i) p.tile_bin[i] = e;
+            for (int i = seg[p.E] / p.align + tid; i < p.max_tiles; i += kSortThreads) p.tile_bin[i] = -1;
+        }
+    }
     // the padding behind each group's entries
     if (p.entry_of && chunk == 0)
         for (int e = warp; e < p.E; e += kSortWarps)
