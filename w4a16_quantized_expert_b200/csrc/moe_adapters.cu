@@ -9,21 +9,28 @@
 // 128 tokens and take the tcgen05 kernels (shrink_tile_kernel, expand_tile_kernel,
 // grad_tile_kernel), and so does every gradient.
 //
-// z enters a second product, whose operands are 16-bit.  It is carried as two pieces
-// hi = T(z c), lo = T(z c - hi) with a power of two c per row (the gradient of the weights:
-// per adapter) that keeps fp16 in range: the product's error stays at fp32's level where a
-// single rounding of z to 16 bits would cost 2^-9 of the result.
+// z enters a second product, whose operands are 16-bit.  It is carried as a sum of pieces,
+// each the rounding of what the ones before leave: two in fp16 (22 bits), under a power of
+// two per row (the gradient of the weights: per adapter) that keeps them in fp16's range;
+// three in bf16 (all 24 bits).  The products' error stays at fp32's level, where a single
+// rounding of z to 16 bits would cost up to 2^-9 of the result and two bf16 pieces 3e-6
+// (measured on weight gradients, against 8e-7 for the same sums in fp32).
 #include "moe_internal.h"
 #include "moe_rows.cuh"
 #include "moe_tcgen05.cuh"
 
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <new>
+#include <type_traits>
 
 // the opaque handle
 struct moe_adapters {
     moe_adapters_desc desc;
     moe_adapters_weights w;
+    // boxes of 64 columns: A [ranks], B [128 rows], B [64 rows]
+    CUtensorMap map_a, map_b, map_b64;
     int *d_status;
     int device;
     int num_sms;
@@ -39,6 +46,9 @@ constexpr int kFewN = 128;         // columns per CTA of the small expand
 constexpr int kTile = 128;         // tokens per tile of the tcgen05 kernels (MMA M)
 constexpr int kBlk = kTile * 128;  // bytes of a [128 rows][64 columns] 16-bit block
 constexpr int kWorkers = 256;      // load and epilogue threads of a tcgen05 CTA
+constexpr int kTcThreads = kWorkers + 32;   // and its MMA warp
+constexpr int kMmaWarp = kWorkers / 32, kTmaWarp = kMmaWarp + 1;
+constexpr size_t kMaxSmem = 224 * 1024;     // of a ring
 constexpr int kMaxSplit = 8;       // CTAs of a cluster that share a contraction
 
 struct AdParams {
@@ -55,8 +65,8 @@ struct AdParams {
     int T, K, N, R, Kp, n, accumulate, want_dw;
     // the plan: tokens sorted by adapter, tiles of 128 positions
     int32_t *seg, *counts, *entry_of, *tile_bin;
-    // intermediates, by position: z (dz) as pieces [2 Kp], the scale that undoes c
-    void *limb, *zl, *dl;
+    // intermediates, by position: z (dz) as pieces [kPieces][Kp], the scale that undoes theirs
+    void *pieces, *zl, *dl;
     float *row_scale, *dz;
     unsigned *amax;              // [2][n] largest |dz|, |z| of each adapter (fp16 pools)
     float *z_part;               // small path: [splits][T][R]
@@ -85,13 +95,29 @@ __device__ __forceinline__ float norm_scale(float m, float &inverse)
 
 __device__ __forceinline__ float finite_or_0(float v) { return fabsf(v) <= 3.4028234663852886e38f ? fabsf(v) : 0.f; }
 
-// v as two pieces; an infinite or NaN piece stands alone
 template <typename T>
-__device__ __forceinline__ void split2(float v, T &hi, T &lo)
+constexpr int kPieces = TcType<T>::code ? 3 : 2;
+
+// v as pieces; an infinite or NaN piece stands alone
+template <typename T>
+__device__ __forceinline__ void split_pieces(float v, T (&piece)[kPieces<T>])
 {
-    hi = from_f32<T>(v);
-    const float h = f32_of(hi);
-    lo = from_f32<T>(fabsf(h) <= 3.4028234663852886e38f ? v - h : 0.f);
+#pragma unroll
+    for (int i = 0; i < kPieces<T>; ++i) {
+        piece[i] = from_f32<T>(v);
+        const float h = f32_of(piece[i]);
+        v = fabsf(h) <= 3.4028234663852886e38f ? v - h : 0.f;
+    }
+}
+
+// the same to a row of pieces, `stride` apart
+template <typename T>
+__device__ __forceinline__ void store_pieces(float v, T *dst, int stride)
+{
+    T piece[kPieces<T>];
+    split_pieces(v, piece);
+#pragma unroll
+    for (int i = 0; i < kPieces<T>; ++i) dst[i * stride] = piece[i];
 }
 
 __device__ __forceinline__ float warp_max(float v)
@@ -223,7 +249,7 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
     constexpr int W = KB * 16;
     __shared__ int s_tok[16];
     __shared__ float s_scale[16], s_z[16][W];
-    __shared__ __align__(8) TX s_hi[16][W], s_lo[16][W];
+    __shared__ __align__(8) TX s_p[kPieces<TX>][16][W];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, tig = lane & 3;
     pdl_trigger();
     int cnt = 0;
@@ -304,10 +330,7 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
         float inv;
         const float c = norm_scale(warp_max(m), inv);
         for (int j = lane; j < W; j += 32) {
-            TX hi, lo;
-            split2(row < cnt && j < p.R ? s_z[row][j] * c : 0.f, hi, lo);
-            s_hi[row][j] = hi;
-            s_lo[row][j] = lo;
+            store_pieces(row < cnt && j < p.R ? s_z[row][j] * c : 0.f, &s_p[0][row][j], 16 * W);
         }
         if (lane == 0) s_scale[row] = inv;
     }
@@ -316,12 +339,12 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
         const int j = k * 16 + tig * 4;
-        const uint2 h0 = *reinterpret_cast<const uint2 *>(&s_hi[g][j]), h1 = *reinterpret_cast<const uint2 *>(&s_hi[g + 8][j]);
-        const uint2 l0 = *reinterpret_cast<const uint2 *>(&s_lo[g][j]), l1 = *reinterpret_cast<const uint2 *>(&s_lo[g + 8][j]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            mma_t<TX>(acc[i], h0.x, h1.x, h0.y, h1.y, bv[i][k].x, bv[i][k].y);
-            mma_t<TX>(acc[i], l0.x, l1.x, l0.y, l1.y, bv[i][k].x, bv[i][k].y);
+        for (int l = 0; l < kPieces<TX>; ++l) {
+            const uint2 z0 = *reinterpret_cast<const uint2 *>(&s_p[l][g][j]);
+            const uint2 z1 = *reinterpret_cast<const uint2 *>(&s_p[l][g + 8][j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_t<TX>(acc[i], z0.x, z1.x, z0.y, z1.y, bv[i][k].x, bv[i][k].y);
         }
     }
 #pragma unroll
@@ -340,48 +363,45 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
 }
 
 // ============================================================================ tiles
-// Ring of shared-memory stages between the load threads and the thread that issues the
-// MMAs.  Every load thread copies its share of a stage with cp.async and reports it kLag
-// stages later, when the copies have landed (one arrival per warp).
+// Ring of shared-memory stages between the load warps and the thread that issues the MMAs.
+// A load thread copies its share of a stage's rows with cp.async (a tile's tokens lie
+// anywhere; row gathers by TMA were slower: 26 against 21 us for the shrink of 4096 tokens of
+// 6144) and reports it kLag steps later, when the copies have landed, with one arrival per
+// warp; the weights' boxes come by TMA and add one arrival.
 template <int NS>
 struct Ring {
     uint64_t full[NS], empty[NS], done;
-    __device__ void init(int warps)
+    __device__ void init(int arrivals)
     {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], warps);
+            mbar_init(&full[i], arrivals);
             mbar_init(&empty[i], 1);
         }
         mbar_init(&done, 1);
-        fence_mbar_init();
     }
 };
 
-// Load loop of one thread: issue(stage, i) starts the copies of step i.  Returns false if a
-// wait gave up.
+// Load loop of one thread: copy(stage, i) starts the copies of step i.
 template <int NS, typename F>
-__device__ __forceinline__ bool ring_load(Ring<NS> &r, int steps, int *status, F &&issue)
+__device__ __forceinline__ void ring_load(Ring<NS> &r, int steps, int *status, F &&copy)
 {
     constexpr int kLag = NS - 1;
-    const int lane = threadIdx.x & 31;
-    bool ok = true;
     for (int i = 0; i < steps + kLag; ++i) {
         if (i < steps) {
-            if (i >= NS && ok) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            issue(i % NS, i);
+            bool ok = true;
+            if (i >= NS) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            copy(i % NS, i);
         }
         cp_async_commit();
         if (i >= kLag) {
             cp_async_wait<kLag>();
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&r.full[(i - kLag) % NS]);
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&r.full[(i - kLag) % NS]);
         }
     }
     cp_async_wait<0>();
-    return ok;
 }
 
 // Issue loop of the MMA thread: mma(stage, i) issues the MMAs of step i.
@@ -397,7 +417,7 @@ __device__ __forceinline__ void ring_mma(Ring<NS> &r, int steps, int *status, F 
     tc_commit(&r.done);
 }
 
-__device__ __forceinline__ uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : 256u; }
+__device__ __forceinline__ uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
 
 constexpr int kShrinkNS = 4;
 
@@ -413,12 +433,13 @@ __host__ __device__ inline int shrink_w_bytes(bool grad, int R, int Kp)
 // the weight gradients the adapters' largest magnitudes (fp16) or z_in's pieces (bf16).
 // Bound by the rows of X.
 template <typename TX, bool kGrad>
-__global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdParams p)
+__global__ void __launch_bounds__(kTcThreads)
+    shrink_tile_kernel(const __grid_constant__ CUtensorMap map_w, const AdParams p)
 {
     extern __shared__ unsigned char raw[];
     __shared__ Ring<kShrinkNS> ring;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_tok[kTile];
+    __shared__ __align__(16) int s_tok[kTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = cluster_size(), q = cluster_rank(), tile = blockIdx.x / S;
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -430,15 +451,18 @@ __global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdPara
     const int32_t *entry = p.entry_of + (size_t)tile * kTile;
     if (rank == 0) {
         if (p.z_out)
-            for (int i = q * (kWorkers + 32) + tid; i < kTile * R; i += S * (kWorkers + 32)) {
+            for (int i = q * kTcThreads + tid; i < kTile * R; i += S * kTcThreads) {
                 const int t = __ldcg(entry + i / R);
                 if (t >= 0) p.z_out[(size_t)t * R + i % R] = 0.f;
             }
         return;
     }
     if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);
-    if (tid == 0) ring.init(kWorkers / 32);
-    if (warp == kWorkers / 32) tc_alloc(&s_tmem, tmem_cols(Kp));
+    if (tid == 0) {
+        ring.init(kWorkers / 32 + 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(Kp));
     tc_before();
     __syncthreads();
     tc_after();
@@ -448,12 +472,10 @@ __global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdPara
     const int b_lo = (int)((long long)blocks * q / S), steps = (int)((long long)blocks * (q + 1) / S) - b_lo;
     const int wb = shrink_w_bytes(kGrad, R, Kp), stage = kBlk + wb;
     const int pitch = Kp + 4;   // floats of a row of the partial sums
-    if (warp < kWorkers / 32) {
+    if (warp < kMmaWarp) {
         const int c = tid & 7, r0 = tid >> 3;
         const TX *X = static_cast<const TX *>(kGrad ? p.dy : p.x);
         const long long ld = kGrad ? p.lddy : p.ldx;
-        const TX *W = kGrad ? static_cast<const TX *>(p.b) + (size_t)bin * p.N * R
-                            : static_cast<const TX *>(p.a) + (size_t)bin * R * p.K;
         const TX *px[4];
         bool live[4];
 #pragma unroll
@@ -463,33 +485,30 @@ __global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdPara
             px[i] = X + (live[i] ? t * ld : 0) + c * 8;
         }
         ring_load<kShrinkNS>(ring, steps, p.status, [&](int s, int i) {
-            const int k0 = (b_lo + i) * 64, k = k0 + c * 8;
+            const int k0 = (b_lo + i) * 64;
             const uint32_t xs = sbuf + s * stage, ws = xs + kBlk;
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-                cp_async16_or_zero(xs + swz(r0 + 32 * u, c), live[u] && k < width ? px[u] + k0 : X, live[u] && k < width);
-            if (kGrad) {
-                for (int u = 0; u < 2; ++u) {
-                    const int kk = r0 + 32 * u;
-                    for (int b = 0; b * 64 < R; ++b) {
-                        const bool in = k0 + kk < width && b * 64 + c * 8 < R;
-                        cp_async16_or_zero(ws + b * 8192 + swz(kk, c), in ? W + (size_t)(k0 + kk) * R + b * 64 + c * 8 : W, in);
-                    }
-                }
-            } else {
-                for (int j = r0; j < Kp; j += 32) {
-                    const bool in = k < width && j < R;
-                    cp_async16_or_zero(ws + swz(j, c), in ? W + (size_t)j * p.K + k : W, in);
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&ring.full[s], wb);
+                if (kGrad) {
+                    tma_box(ws, &map_w, &ring.full[s], 0, k0, bin);
+                    if (R > 64) tma_box(ws + 8192, &map_w, &ring.full[s], 64, k0, bin);
+                } else {
+                    tma_box(ws, &map_w, &ring.full[s], k0, 0, bin);
                 }
             }
+            const bool in = k0 + c * 8 < width;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                cp_async16_or_zero(xs + swz(r0 + 32 * u, c), live[u] && in ? px[u] + k0 : X, live[u] && in);
         });
         mbar_wait(&ring.done, 0, p.status);
+        __syncwarp();
         tc_after();
         float *P = reinterpret_cast<float *>(buf);
         const int row = (warp & 3) * 32 + lane, half = warp >> 2;
         for (int col = half * (Kp / 2); col < (half + 1) * (Kp / 2); col += 8) {
             float v[8];
-            tc_ld8(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
+            tc_ld(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
             tc_wait_ld();
             float4 *dst = reinterpret_cast<float4 *>(P + row * pitch + col);
             dst[0] = make_float4(v[0], v[1], v[2], v[3]);
@@ -509,10 +528,10 @@ __global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdPara
     __syncwarp();
     if (S > 1) cluster_sync();
     else __syncthreads();
-    if (warp == kWorkers / 32) {
+    if (warp == kMmaWarp) {
         tc_after();
         tc_dealloc(tmem, tmem_cols(Kp));
-    } else {
+    } else if (warp < kMmaWarp) {
         const int per = kTile / S;
         const float scaling = kGrad ? __ldcg(p.scaling + bin) : 1.f;
         const float apply_scale = kGrad ? 1.f : __ldcg(p.scaling + bin);
@@ -540,28 +559,25 @@ __global__ void __launch_bounds__(kWorkers + 32) shrink_tile_kernel(const AdPara
             m = warp_max(m);
             float inv;
             const float c = norm_scale(m, inv);
-            TX *limb = static_cast<TX *>(p.limb) + pos * 2 * Kp;
+            TX *pieces = static_cast<TX *>(p.pieces) + pos * kPieces<TX> * Kp;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int col = lane + 32 * i;
                 if (col >= Kp) continue;
-                TX hi, lo;
-                split2(v[i] * (TcType<TX>::code ? 1.f : c), hi, lo);   // (bf16 has fp32's range)
-                limb[col] = hi;
-                limb[Kp + col] = lo;
+                store_pieces(v[i] * (TcType<TX>::code ? 1.f : c), pieces + col, Kp);   // (bf16 has fp32's range)
                 if (p.z_out && tok >= 0 && col < R) p.z_out[(size_t)tok * R + col] = v[i];
                 if (kGrad && p.want_dw && !TcType<TX>::code && col < R) p.dz[pos * R + col] = v[i];
             }
             if (lane == 0) p.row_scale[pos] = (TcType<TX>::code ? 1.f : inv) * apply_scale;
             if (kGrad && p.want_dw) {
                 float zm = 0.f;
-                TX *zl = static_cast<TX *>(p.zl) + pos * 2 * Kp;
+                TX *zl = static_cast<TX *>(p.zl) + pos * kPieces<TX> * Kp;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int col = lane + 32 * i;
                     const float z = col < rank && tok >= 0 ? __ldcg(p.z_in + (size_t)tok * R + col) : 0.f;
                     if (TcType<TX>::code) {
-                        if (col < Kp) split2(z, zl[col], zl[Kp + col]);
+                        if (col < Kp) store_pieces(z, zl + col, Kp);
                     } else {
                         zm = fmaxf(zm, finite_or_0(z));
                     }
@@ -596,27 +612,30 @@ __global__ void __launch_bounds__(kWorkers) pieces_kernel(const AdParams p)
     float inv;
     const float cd = norm_scale(__uint_as_float(__ldcg(p.amax + bin)), inv);
     const float cz = norm_scale(__uint_as_float(__ldcg(p.amax + p.n + bin)), inv);
-    __half *dl = static_cast<__half *>(p.dl) + pos * 2 * p.Kp, *zl = static_cast<__half *>(p.zl) + pos * 2 * p.Kp;
+    const size_t row = pos * kPieces<__half> * p.Kp;
+    __half *dl = static_cast<__half *>(p.dl) + row, *zl = static_cast<__half *>(p.zl) + row;
     for (int col = lane; col < p.Kp; col += 32) {
         const bool in = col < rank && tok >= 0;
-        split2(in ? __ldcg(p.dz + pos * p.R + col) * cd : 0.f, dl[col], dl[p.Kp + col]);
-        split2(in ? __ldcg(p.z_in + (size_t)tok * p.R + col) * cz : 0.f, zl[col], zl[p.Kp + col]);
+        store_pieces(in ? __ldcg(p.dz + pos * p.R + col) * cd : 0.f, dl + col, p.Kp);
+        store_pieces(in ? __ldcg(p.z_in + (size_t)tok * p.R + col) * cz : 0.f, zl + col, p.Kp);
     }
 }
 
 // da[a][j][k] = sum_t dz[t][j] x[t][k] and db[a][n][j] = s sum_t z[t][j] dy[t][n]: one product
 // D[c][j] = sum_t X[t][c] Z[t][j] over an adapter's tokens, 128 columns c of X per cluster,
 // its tokens dealt to the S CTAs 64 at a time.  Both operands are MN-major (rows are
-// tokens); Z's two pieces lie side by side as 2 Kp columns of one MMA.  The CTAs' parts meet
+// tokens); Z's pieces lie side by side as the columns
+// of one MMA (two MMAs past 256 columns).  The CTAs' parts meet
 // as in the shrink kernel.  Bound by reading X.
-constexpr int kGradNS = 4;
-__host__ __device__ inline int grad_z_bytes(int Kp) { return (2 * Kp + 63) / 64 * 8192; }
+__host__ __device__ inline int grad_z_bytes(int cols) { return (cols + 63) / 64 * 8192; }
 
-template <typename TX>
-__global__ void __launch_bounds__(kWorkers + 32) grad_tile_kernel(const AdParams p)
+template <typename TX, int NS>
+__global__ void __launch_bounds__(kTcThreads)
+    grad_tile_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_z,
+                     const AdParams p)
 {
     extern __shared__ unsigned char raw[];
-    __shared__ Ring<kGradNS> ring;
+    __shared__ Ring<NS> ring;
     __shared__ uint32_t s_tmem;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int S = cluster_size(), q = cluster_rank();
@@ -626,84 +645,103 @@ __global__ void __launch_bounds__(kWorkers + 32) grad_tile_kernel(const AdParams
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
     pdl_trigger();
-    const int R = p.R, Kp = p.Kp, rank = rank_of(p, a);
+    const int R = p.R, Kp = p.Kp, ZC = kPieces<TX> * Kp, rank = rank_of(p, a);
     const int cnt = rank ? __ldcg(p.counts + a) : 0;
     float *out = is_b ? p.db + ((size_t)a * p.N + c0) * R : p.da + (size_t)a * R * p.K + c0;
     const int cols = min(128, width - c0);
     if (cnt == 0) {   // (the whole cluster)
         if (p.accumulate) return;
         if (is_b) {
-            for (int i = q * (kWorkers + 32) + tid; i < cols * R; i += S * (kWorkers + 32)) out[i] = 0.f;
+            for (int i = q * kTcThreads + tid; i < cols * R; i += S * kTcThreads) out[i] = 0.f;
         } else {
-            for (int i = q * (kWorkers + 32) + tid; i < 128 * R; i += S * (kWorkers + 32))
+            for (int i = q * kTcThreads + tid; i < 128 * R; i += S * kTcThreads)
                 if ((i & 127) < cols) out[(size_t)(i >> 7) * p.K + (i & 127)] = 0.f;
         }
         return;
     }
     const size_t pos0 = (size_t)__ldcg(p.seg + a);
-    if (tid == 0) ring.init(kWorkers / 32);
-    if (warp == kWorkers / 32) tc_alloc(&s_tmem, tmem_cols(2 * Kp));
+    if (tid == 0) {
+        ring.init(kWorkers / 32 + 1);
+        fence_mbar_init();
+    }
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(ZC));
     tc_before();
     __syncthreads();
     tc_after();
     const uint32_t tmem = s_tmem, sbuf = smem_u32(buf);
     const int blocks = (cnt + 63) / 64, steps = (blocks - q + S - 1) / S;   // token blocks q, q + S, ..
-    const int stage = 2 * 8192 + grad_z_bytes(Kp);
+    const int stage = 2 * 8192 + grad_z_bytes(ZC);
     const int pitch = is_b ? Kp + 4 : 128 + 4;
     float *P = reinterpret_cast<float *>(buf);
-    if (warp < kWorkers / 32) {
+    if (warp < kMmaWarp) {
         const TX *X = static_cast<const TX *>(is_b ? p.dy : p.x);
+        const CUtensorMap *mz = is_b ? &map_z : &map_dz;
         const long long ld = is_b ? p.lddy : p.ldx;
-        const TX *Z = static_cast<const TX *>(is_b ? p.zl : p.dl);
-        const int cx = tid & 15, rx = tid >> 4, ch = Kp / 4;   // 16-byte chunks of a row of Z
-        ring_load<kGradNS>(ring, steps, p.status, [&](int s, int i) {
-            const size_t pos = pos0 + (size_t)(q + i * S) * 64;
-            const uint32_t xs = sbuf + s * stage, zs = xs + 2 * 8192;
+        const int cx = tid & 15, rx = tid >> 4;   // 16-byte chunk of a row, first of four rows
+        const bool in_x = cx * 8 < cols;
+        const TX *Xc = X + c0 + cx * 8;
+        const int32_t *ids = p.entry_of + pos0 + q * 64 + rx;
+        int t[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t[u] = steps > 0 ? __ldcg(ids + 16 * u) : -1;
+        ring_load<NS>(ring, steps, p.status, [&](int s, int i) {
+            const uint32_t xs = sbuf + s * stage + (cx >> 3) * 8192, zs = sbuf + s * stage + 2 * 8192;
+            if (tid == 0) {
+                mbar_arrive_expect_tx(&ring.full[s], stage - 2 * 8192);
+                for (int c = 0; c * 64 < ZC; ++c)
+                    tma_box2(zs + c * 8192, mz, &ring.full[s], c * 64, (int)pos0 + (q + i * S) * 64);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int row = rx + 16 * u, t = __ldcg(p.entry_of + pos + row);
-                const bool in = t >= 0 && cx * 8 < cols;
-                cp_async16_or_zero(xs + (cx >> 3) * 8192 + swz(row, cx & 7), in ? X + t * ld + c0 + cx * 8 : X, in);
+                const bool in = t[u] >= 0 && in_x;
+                cp_async16_or_zero(xs + swz(rx + 16 * u, cx & 7), in ? Xc + t[u] * ld : X, in);
             }
-            for (int e = tid; e < 64 * ch; e += kWorkers) {
-                const int row = e / ch, c = e % ch;
-                cp_async16_or_zero(zs + (c >> 3) * 8192 + swz(row, c & 7), Z + (pos + row) * 2 * Kp + c * 8, true);
-            }
+            if (i + 1 < steps)   // the next step's tokens, a step ahead
+#pragma unroll
+                for (int u = 0; u < 4; ++u) t[u] = __ldcg(ids + (size_t)(i + 1) * S * 64 + 16 * u);
         });
         if (steps > 0) mbar_wait(&ring.done, 0, p.status);
+        __syncwarp();
         tc_after();
         const int c = (warp & 3) * 32 + lane, half = warp >> 2;
         for (int j = half * (Kp / 2); j < (half + 1) * (Kp / 2); j += 8) {
-            float v[8] = {}, w[8] = {};
+            float v[kPieces<TX>][8] = {};
             if (steps > 0) {
-                const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + j;
-                tc_ld8(t, v);
-                tc_ld8(t + Kp, w);
+#pragma unroll
+                for (int l = 0; l < kPieces<TX>; ++l)
+                    tc_ld(tmem + ((uint32_t)((warp & 3) * 32) << 16) + l * Kp + j, v[l]);
                 tc_wait_ld();
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                if (is_b) P[c * pitch + j + e] = v[e] + w[e];
-                else P[(j + e) * pitch + c] = v[e] + w[e];
+                float sum = v[kPieces<TX> - 1][e];   // (the smallest first)
+#pragma unroll
+                for (int l = kPieces<TX> - 2; l >= 0; --l) sum += v[l][e];
+                if (is_b) P[c * pitch + j + e] = sum;
+                else P[(j + e) * pitch + c] = sum;
             }
         }
         tc_before();
     } else if (lane == 0 && steps > 0) {
-        const uint32_t idesc = idesc16<TX>(2 * Kp, true, true);
-        ring_mma<kGradNS>(ring, steps, p.status, [&](int s, int i) {
+        const uint32_t idesc = idesc16<TX>(min(ZC, 256), true, true), idesc2 = idesc16<TX>(ZC - 256, true, true);
+        ring_mma<NS>(ring, steps, p.status, [&](int s, int i) {
             const uint32_t xs = sbuf + s * stage;
             const uint64_t da = sdesc_mn(xs, 8192), db = sdesc_mn(xs + 2 * 8192, 8192);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) tc_mma16(tmem, da + 128 * kk, db + 128 * kk, idesc, i > 0 || kk > 0);
+            for (int kk = 0; kk < 4; ++kk) {
+                tc_mma16(tmem, da + 128 * kk, db + 128 * kk, idesc, i > 0 || kk > 0);
+                if (ZC > 256)   // (columns 256 .. start at block 4)
+                    tc_mma16(tmem + 256, da + 128 * kk, db + 4 * 512 + 128 * kk, idesc2, i > 0 || kk > 0);
+            }
         });
     }
     __syncwarp();
     if (S > 1) cluster_sync();
     else __syncthreads();
-    if (warp == kWorkers / 32) {
+    if (warp == kMmaWarp) {
         tc_after();
-        tc_dealloc(tmem, tmem_cols(2 * Kp));
-    } else {
+        tc_dealloc(tmem, tmem_cols(ZC));
+    } else if (warp < kMmaWarp) {
         float scale = is_b ? __ldcg(p.scaling + a) : 1.f, inv = 1.f;
         if (!TcType<TX>::code) {
             norm_scale(__uint_as_float(__ldcg(p.amax + (is_b ? p.n : 0) + a)), inv);
@@ -743,32 +781,336 @@ __global__ void __launch_bounds__(kWorkers + 32) grad_tile_kernel(const AdParams
     if (S > 1) cluster_sync();
 }
 
-// y[t][n] = y_in[t][n] + sum_j z[t][j] B[n][j] (kGrad: dx = dx_in + dz A) of one tile of 128
-// tokens and a run of 128-column blocks.  Operands: z's pieces [128 tokens][2 Kp] K-major,
-// loaded once; B [128 n][ranks] K-major, or A [ranks][128 k] MN-major, two stages; D double
-// buffered in TMEM.  Eight epilogue warps (32 rows x 64 columns each) turn D's rows into
-// coalesced rows through shared memory and add y_in, loaded ahead of the product.  Bound by
-// reading y_in and writing y.
-constexpr int kExpandThreads = kWorkers + 32 + 64;   // epilogue, MMA, load warps
-constexpr int kScratch = 32 * 36 * 4;                // a warp's 32 x 32 block, padded rows
+// y[t][n] = y_in[t][n] + sum_j z[t][j] B[n][j] (kGrad: dx = dx_in + dz A), whose rows are 16-byte
+// aligned.  A persistent CTA per SM takes a run of (tile, block of 128 columns) items.
+// Operands: z's pieces [128 tokens][pieces x Kp] K-major, loaded once per tile; B [columns]
+// [ranks] K-major, or A [ranks][columns] MN-major, two stages; both by TMA; D in TMEM, double
+// buffered.  Eight epilogue warps (32 tokens x 64 columns each) turn D's rows (a TMEM lane is
+// a token) into coalesced rows through shared memory, 32 columns at a time, and add y_in,
+// whose loads run 64 KB ahead per SM.  Bound by reading y_in and writing y.  Measured for
+// 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): EXPAND_US us;
+// a lane per token straight to memory 67 us and a lane per column 44 us (the load/store
+// unit), TMA row gathers and scatters 62 us (about 75 cycles per four rows).
+constexpr int kExpandThreads = kWorkers + 96;   // epilogue, MMA, TMA, fix warps
+constexpr int kExpandNS = 3;
+constexpr int kMaxRun = 16;                     // tiles that a CTA's run may touch
+constexpr int kPitch = 36;                      // floats of a row of an epilogue warp's block
 
-__host__ __device__ inline int expand_z_bytes(int Kp) { return (2 * Kp + 63) / 64 * kBlk; }
-__host__ __device__ inline int expand_w_bytes(bool grad, int Kp) { return grad ? Kp * 256 : (Kp + 63) / 64 * kBlk; }
+__host__ __device__ inline int expand_z_bytes(int cols) { return (cols + 63) / 64 * kBlk; }
+// bytes of a weight stage of n columns of the output
+__host__ __device__ inline int expand_w_bytes(bool grad, int Kp, int n) { return grad ? Kp * 2 * n : (Kp + 63) / 64 * n * 128; }
 
-template <typename TX, typename TY, bool kGrad, bool kVec>
-__global__ void __launch_bounds__(kExpandThreads, 1) expand_tile_kernel(const AdParams p)
+// Zeros the entries [rank, next multiple of 16) of a weight stage of n output columns: rows
+// of an MN-major stage, columns of a K-major one.
+template <bool kGrad>
+__device__ __forceinline__ void zero_past_rank(unsigned char *w, int rank, int Kp, int n, int lane)
+{
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const int end = (rank + 15) & ~15;
+    if (kGrad) {
+        const int ch = n / 8;
+        for (int e = lane; e < (end - rank) * ch; e += 32) {
+            const int j = rank + e / ch, c = e % ch;
+            *reinterpret_cast<uint4 *>(w + (c >> 3) * (Kp * 128) + swz(j, c & 7)) = zero;
+        }
+        return;
+    }
+    const int c = rank >> 3, rest = rank & 7, c1 = rest ? c + 1 : c;
+    for (int row = lane; row < n; row += 32) {
+        if (rest) {
+            uint4 *q = reinterpret_cast<uint4 *>(w + (c >> 3) * n * 128 + swz(row, c & 7));
+            uint4 v = *q;
+            uint32_t *f = &v.x;
+#pragma unroll
+            for (int h = 0; h < 4; ++h) f[h] &= rest >= 2 * h + 2 ? 0xFFFFFFFFu : rest == 2 * h + 1 ? 0xFFFFu : 0u;
+            *q = v;
+        }
+        if (c1 * 8 < end) *reinterpret_cast<uint4 *>(w + (c1 >> 3) * n * 128 + swz(row, c1 & 7)) = zero;
+    }
+}
+
+// adds to two neighbouring 16-bit elements, or to one fp32
+template <typename TY>
+__device__ __forceinline__ uint32_t add_pair(uint32_t base, float a, float b);
+template <>
+__device__ __forceinline__ uint32_t add_pair<__half>(uint32_t base, float a, float b)
+{
+    const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&base));
+    const __half2 r = __floats2half2_rn(f.x + a, f.y + b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t add_pair<__nv_bfloat16>(uint32_t base, float a, float b)
+{
+    const __nv_bfloat162 r = __floats2bfloat162_rn(__uint_as_float(base << 16) + a,
+                                                   __uint_as_float(base & 0xFFFF0000u) + b);
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+template <>
+__device__ __forceinline__ uint32_t add_pair<float>(uint32_t base, float a, float)
+{
+    return __float_as_uint(__uint_as_float(base) + a);
+}
+
+template <typename TX, typename TY, bool kGrad>
+__global__ void __launch_bounds__(kExpandThreads, 1)
+    expand_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_z,
+                       const AdParams p)
 {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t wfull[2], wempty[2], tfull[2], tempty[2];
+    __shared__ uint64_t zfull, zempty, wland[2], wfull[2], wempty[2], tfull[2], tempty[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_bin[kMaxRun], s_rank[kMaxRun];
+    __shared__ int s_tok[kMaxRun * kTile];
+    __shared__ float s_scale[kMaxRun * kTile];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    if (tid == 0) {
+        mbar_init(&zfull, 1);
+        mbar_init(&zempty, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&wland[i], 1);
+            mbar_init(&wfull[i], 1);
+            mbar_init(&wempty[i], 1);
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], kWorkers / 32);
+        }
+        fence_mbar_init();
+    }
+    pdl_wait();
+    pdl_trigger();
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, 256);
+    const int Kp = p.Kp, ZC = kPieces<TX> * Kp, width = kGrad ? p.K : p.N;
+    const int zb = expand_z_bytes(ZC), wb = expand_w_bytes(kGrad, Kp, 128);
+    const int nt_all = (width + 127) / 128;
+    const long long items = (long long)(__ldcg(p.seg + p.n + 1) / kTile) * nt_all;
+    const int lo = (int)(items * blockIdx.x / gridDim.x), hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
+    // the run's tiles: adapters, ranks, tokens, scales
+    const int tile0 = lo / nt_all, run = hi > lo ? (hi - 1) / nt_all - tile0 + 1 : 0;
+    for (int i = tid; i < run; i += kExpandThreads) {
+        s_bin[i] = __ldcg(p.tile_bin + tile0 + i);
+        s_rank[i] = rank_of(p, s_bin[i]);
+    }
+    for (int i = tid; i < run * kTile; i += kExpandThreads) {
+        s_tok[i] = __ldcg(p.entry_of + (size_t)tile0 * kTile + i);
+        s_scale[i] = __ldcg(p.row_scale + (size_t)tile0 * kTile + i);
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t zs = smem_u32(buf), ws = zs + zb, tmem = s_tmem;
+    const TY *in = static_cast<const TY *>(p.y_in);
+    TY *y = static_cast<TY *>(p.y);
+    // every role walks the same items; j counts the ones that have a product, zc their tiles
+    int cur = -1, j = 0, zc = 0;
+    if (warp == kTmaWarp) {   // ---- copies of the operands
+        if (lane == 0)
+            for (int it = lo; it < hi; ++it) {
+                const int lt = it / nt_all - tile0, n0 = it % nt_all * 128, s = j & 1;
+                if (!s_rank[lt]) continue;
+                if (lt != cur) {
+                    cur = lt;
+                    if (zc && !mbar_wait(&zempty, (zc - 1) & 1, p.status)) break;
+                    mbar_arrive_expect_tx(&zfull, zb);
+                    for (int b = 0; b * kBlk < zb; ++b)
+                        for (int r = 0; r < kTile; r += 64)
+                            tma_box2(zs + b * kBlk + r * 128, &map_z, &zfull, b * 64, (tile0 + lt) * kTile + r);
+                    ++zc;
+                }
+                if (j >= 2 && !mbar_wait(&wempty[s], ((j >> 1) & 1) ^ 1, p.status)) break;
+                const uint32_t w = ws + s * wb;
+                mbar_arrive_expect_tx(&wland[s], wb);
+                if (kGrad) {
+                    tma_box(w, &map_w, &wland[s], n0, 0, s_bin[lt]);
+                    tma_box(w + Kp * 128, &map_w, &wland[s], n0 + 64, 0, s_bin[lt]);
+                } else {
+                    tma_box(w, &map_w, &wland[s], 0, n0, s_bin[lt]);
+                    if (Kp > 64) tma_box(w + kBlk, &map_w, &wland[s], 64, n0, s_bin[lt]);
+                }
+                ++j;
+            }
+    } else if (warp == kTmaWarp + 1) {
+        // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
+        // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
+        for (int it = lo; it < hi; ++it) {
+            const int rank = s_rank[it / nt_all - tile0], s = j & 1;
+            if (!rank) continue;
+            const bool ok = mbar_wait(&wland[s], (j >> 1) & 1, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (rank & 15) {
+                zero_past_rank<kGrad>(buf + zb + s * wb, rank, Kp, 128, lane);
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(&wfull[s]);
+            ++j;
+        }
+    } else if (warp == kMmaWarp) {   // ---- products
+        if (lane == 0) {
+            const uint32_t idesc = idesc16<TX>(128, false, kGrad);
+            for (int it = lo; it < hi; ++it) {
+                const int lt = it / nt_all - tile0, rank = s_rank[lt], s = j & 1;
+                if (!rank) continue;
+                if (lt != cur) {
+                    cur = lt;
+                    if (zc) tc_commit(&zempty);   // the tile before is done with z
+                    if (!mbar_wait(&zfull, zc & 1, p.status)) break;
+                    ++zc;
+                }
+                if (!mbar_wait(&wfull[s], (j >> 1) & 1, p.status)) break;
+                if (j >= 2 && !mbar_wait(&tempty[s], ((j >> 1) & 1) ^ 1, p.status)) break;
+                tc_after();
+                const uint32_t w = ws + s * wb;
+                for (int l = 0; l < kPieces<TX>; ++l)
+                    for (int k = 0; k < rank; k += 16) {
+                        const int at = l * Kp + k;
+                        const uint64_t dz = sdesc_k(zs + (at >> 6) * kBlk) + ((at & 63) >> 3);
+                        const uint64_t dw = kGrad ? sdesc_mn(w, Kp * 128) + 8 * k : sdesc_k(w + (k >> 6) * kBlk) + ((k & 63) >> 3);
+                        tc_mma16(tmem + s * 128, dz, dw, idesc, at > 0);
+                    }
+                tc_commit(&wempty[s]);
+                tc_commit(&tfull[s]);
+                ++j;
+            }
+        }
+    } else {   // ---- epilogue: tokens [32 q4, +32), columns [64 half, +64)
+        const int q4 = warp & 3, half = warp >> 2;
+        float *sc = reinterpret_cast<float *>(buf + zb + 2 * wb) + warp * 32 * kPitch;
+        constexpr int CE = 16 / sizeof(TY);           // elements of a 16-byte access
+        constexpr int LPR = 32 / CE, NA = LPR;        // lanes of a row, accesses of a 32 x 32 pass
+        constexpr int kItems = sizeof(TY) == 2 ? 2 : 1;   // items whose y_in is in flight: 8 KB a warp
+        const int rl = lane / LPR, cl = lane % LPR * CE;
+        uint4 pre[kItems][2][NA];
+        auto row_token = [&](int it, int a) { return s_tok[(it / nt_all - tile0) * kTile + q4 * 32 + a * (32 / LPR) + rl]; };
+        auto fetch = [&](int it, int ps, uint4 (&v)[NA]) {
+            const int n = it % nt_all * 128 + half * 64 + ps * 32 + cl;
+            if (!in || it >= hi || n >= width) return;
+#pragma unroll
+            for (int a = 0; a < NA; ++a) {
+                const int t = row_token(it, a);
+                if (t >= 0) v[a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
+            }
+        };
+#pragma unroll
+        for (int u = 0; u < kItems; ++u)
+#pragma unroll
+            for (int ps = 0; ps < 2; ++ps) {
+#pragma unroll
+                for (int a = 0; a < NA; ++a) pre[u][ps][a] = make_uint4(0u, 0u, 0u, 0u);
+                fetch(lo + u, ps, pre[u][ps]);
+            }
+        bool ok = true;
+        for (int it0 = lo; it0 < hi && ok; it0 += kItems)
+#pragma unroll
+            for (int u = 0; u < kItems; ++u) {
+                const int it = it0 + u;
+                if (it >= hi || !ok) continue;
+                const int lt = it / nt_all - tile0, s = j & 1;
+                const bool product = s_rank[lt] > 0;
+                if (product) {
+                    ok = mbar_wait(&tfull[s], (j >> 1) & 1, p.status);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) continue;
+                    tc_after();
+                    ++j;
+                }
+                const float scale = s_scale[lt * kTile + q4 * 32 + lane];
+#pragma unroll
+                for (int ps = 0; ps < 2; ++ps) {
+                    const int n = it % nt_all * 128 + half * 64 + ps * 32 + cl;
+                    uint4 o[NA];
+                    if (product) {
+                        float v[32];
+                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + s * 128 + half * 64 + ps * 32, v);
+                        tc_wait_ld();
+                        if (ps == 1) {
+                            tc_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(&tempty[s]);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(sc + lane * kPitch + e) =
+                                make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
+                        __syncwarp();
+#pragma unroll
+                        for (int a = 0; a < NA; ++a) {
+                            const float *d = sc + (a * (32 / LPR) + rl) * kPitch + cl;
+                            uint32_t *f = &o[a].x;
+                            const uint32_t *base = &pre[u][ps][a].x;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (sizeof(TY) == 4) f[e] = add_pair<TY>(base[e], d[e], 0.f);
+                                else f[e] = add_pair<TY>(base[e], d[2 * e], d[2 * e + 1]);
+                            }
+                        }
+                        __syncwarp();
+                    } else {   // no product: the base's bits
+#pragma unroll
+                        for (int a = 0; a < NA; ++a) o[a] = pre[u][ps][a];
+                    }
+                    fetch(it + kItems, ps, pre[u][ps]);
+                    if ((product || in != y) && n < width)
+#pragma unroll
+                        for (int a = 0; a < NA; ++a) {
+                            const int t = row_token(it, a);
+                            if (t >= 0) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o[a];
+                        }
+                }
+            }
+        tc_before();
+    }
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_after();
+        tc_dealloc(tmem, 256);
+    }
+}
+
+// The same for rows of any element alignment, a CTA per tile and run of 128-column blocks.
+// The product is D[n][t]: a TMEM lane is a column of y, so a warp's 32 lanes touch
+// neighbouring elements of a token's row without passing through shared memory.
+
+// The base's bits of a tile's tokens (zeros without a base), eight accesses in flight
+template <typename C, typename TY>
+__device__ void copy_rows(const int *tok, const TY *in, long long ld_in, TY *y, long long ldy, int cols)
+{
+    constexpr int CE = sizeof(C) / sizeof(TY), kU = 8;
+    const int per = cols / CE, n = kTile * per;
+    for (int e0 = threadIdx.x; e0 < n; e0 += kU * kExpandThreads) {
+        C v[kU];
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int e = e0 + u * kExpandThreads, t = e < n ? tok[e / per] : -1;
+            v[u] = C{};
+            if (in && t >= 0) v[u] = *reinterpret_cast<const C *>(in + t * ld_in + e % per * CE);
+        }
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+            const int e = e0 + u * kExpandThreads, t = e < n ? tok[e / per] : -1;
+            if (t >= 0) *reinterpret_cast<C *>(y + t * ldy + e % per * CE) = v[u];
+        }
+    }
+}
+
+// kPair: rows of 16-bit elements start at 4-byte boundaries, and two lanes share a 4-byte
+// access of neighbouring columns (one takes the even token, the other the odd one)
+template <typename TX, typename TY, bool kGrad, bool kPair>
+__global__ void __launch_bounds__(kExpandThreads, 2)
+    expand_any_kernel(const __grid_constant__ CUtensorMap map, const AdParams p)
+{
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t landed[kExpandNS], full[kExpandNS], empty[kExpandNS], tfull[2], tempty[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_tok[kTile];
+    __shared__ __align__(16) float s_scale[kTile];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tile = blockIdx.x;
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
     pdl_trigger();
     const int bin = __ldcg(p.tile_bin + tile);
     if (bin < 0) return;
-    const int rank = rank_of(p, bin), R = p.R, Kp = p.Kp, width = kGrad ? p.K : p.N;
+    const int rank = rank_of(p, bin), Kp = p.Kp, ZC = kPieces<TX> * Kp, width = kGrad ? p.K : p.N;
     const int nt_all = (width + 127) / 128;
     const int nt0 = (int)((long long)nt_all * blockIdx.y / gridDim.y);
     const int nts = (int)((long long)nt_all * (blockIdx.y + 1) / gridDim.y) - nt0;
@@ -778,32 +1120,37 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tile_kernel(const Ad
     if (rank == 0) {
         if (in == y) return;   // in place: nothing to add
         __syncthreads();
-        const int lo = nt0 * 128, hi = min((nt0 + nts) * 128, width);
-        for (int r = warp; r < kTile; r += kExpandThreads / 32) {
-            const int t = s_tok[r];
-            if (t < 0) continue;
-            for (int c = lo + lane; c < hi; c += 32) y[t * p.ldy + c] = in ? in[t * p.ldy_in + c] : from_f32<TY>(0.f);
-        }
+        const int lo = nt0 * 128, cols = min((nt0 + nts) * 128, width) - lo;
+        auto wide = [](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * sizeof(TY) % 16 == 0; };
+        if (wide(y, p.ldy) && (!in || wide(in, p.ldy_in)) && cols * sizeof(TY) % 16 == 0)
+            copy_rows<uint4, TY>(s_tok, in ? in + lo : nullptr, p.ldy_in, y + lo, p.ldy, cols);
+        else
+            copy_rows<typename std::conditional<sizeof(TY) == 4, uint32_t, uint16_t>::type, TY>(
+                s_tok, in ? in + lo : nullptr, p.ldy_in, y + lo, p.ldy, cols);
         return;
     }
-    const uint32_t zs = smem_u32(buf), ws = zs + expand_z_bytes(Kp), wb = expand_w_bytes(kGrad, Kp);
+    const uint32_t zs = smem_u32(buf), ws = zs + expand_z_bytes(ZC), wb = expand_w_bytes(kGrad, Kp, 128);
+    const bool fix = rank & 15;
     if (tid == 0) {
+        for (int i = 0; i < kExpandNS; ++i) {
+            mbar_init(&landed[i], 1);
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&wfull[i], 2);
-            mbar_init(&wempty[i], 1);
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], kWorkers / 32);
         }
         fence_mbar_init();
     }
     if (warp == kWorkers / 32) tc_alloc(&s_tmem, 256);
-    if (warp < kWorkers / 32) {   // z's pieces: chunk i of a row is columns 8 i ..
-        const TX *Z = static_cast<const TX *>(p.limb) + (size_t)tile * kTile * 2 * Kp;
-        const int ch = Kp / 4;
-        for (int e = tid; e < kTile * ch; e += kWorkers) {
-            const int row = e / ch, c = e % ch;
-            cp_async16_or_zero(zs + (c >> 3) * kBlk + swz(row, c & 7), Z + (size_t)row * 2 * Kp + c * 8, true);
-        }
+    if (warp < kWorkers / 32) {   // z's pieces: chunk c of a row is columns 8 c ..
+        const TX *Z = static_cast<const TX *>(p.pieces) + (size_t)tile * kTile * ZC;
+        const int ch = ZC / 8;
+        for (int c = tid & 7; c < ch; c += 8)
+            for (int row = tid >> 3; row < kTile; row += kWorkers / 8)
+                cp_async16_or_zero(zs + (c >> 3) * kBlk + swz(row, c & 7), Z + (size_t)row * ZC + c * 8, true);
+        if (tid < kTile) s_scale[tid] = __ldcg(p.row_scale + (size_t)tile * kTile + tid);
         cp_async_commit();
         cp_async_wait<0>();
         fence_async_smem();
@@ -812,143 +1159,141 @@ __global__ void __launch_bounds__(kExpandThreads, 1) expand_tile_kernel(const Ad
     __syncthreads();
     tc_after();
     const uint32_t tmem = s_tmem;
-    if (warp > kWorkers / 32) {   // ---- weights
-        const int lt = tid - (kWorkers + 32);
-        const TX *W = kGrad ? static_cast<const TX *>(p.a) + (size_t)bin * R * p.K
-                            : static_cast<const TX *>(p.b) + (size_t)bin * p.N * R;
-        const int ch = Kp / 8;
-        bool ok = true;
-        for (int i = 0; i < nts && ok; ++i) {
-            const int s = i & 1, n0 = (nt0 + i) * 128;
+    if (warp == kWorkers / 32 + 1) {   // ---- weights
+        // ---- and the next block's y_in into L2: what the epilogue's registers can keep in
+        // flight covers the latency of L2, not of HBM
+        int tok[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) tok[u] = s_tok[lane + 32 * u];
+        auto prefetch = [&](int i) {
+            const int n0 = (nt0 + i) * 128;
+            if (!in || i >= nts) return;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < 128; c += 128 / (int)sizeof(TY))
+                    if (tok[u] >= 0 && n0 + c < width)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(in + tok[u] * p.ldy_in + n0 + c));
+        };
+        prefetch(0);
+        prefetch(1);
+        for (int i = 0; i < nts; ++i) {
+            const int s = i % kExpandNS, n0 = (nt0 + i) * 128;
             const uint32_t w = ws + s * wb;
-            if (i >= 2) ok = mbar_wait(&wempty[s], ((i >> 1) & 1) ^ 1, p.status);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            if (kGrad) {   // rows past the rank become zeros: they meet z's zeros in the product
-                for (int e = lt; e < Kp * 16; e += 64) {
-                    const int j = e >> 4, c = e & 15;
-                    const bool v = j < rank && n0 + c * 8 < width;
-                    cp_async16_or_zero(w + (c >> 3) * (Kp * 128) + swz(j, c & 7), v ? W + (size_t)j * p.K + n0 + c * 8 : W, v);
+            bool ok = true;
+            if (i >= kExpandNS) ok = mbar_wait(&empty[s], ((i / kExpandNS) & 1) ^ 1, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&landed[s], wb);
+                if (kGrad) {
+                    tma_box(w, &map, &landed[s], n0, 0, bin);
+                    tma_box(w + Kp * 128, &map, &landed[s], n0 + 64, 0, bin);
+                } else {
+                    tma_box(w, &map, &landed[s], 0, n0, bin);
+                    if (Kp > 64) tma_box(w + kBlk, &map, &landed[s], 64, n0, bin);
                 }
-                cp_async_commit();
-                cp_async_wait<0>();
-            } else {
-                for (int e = lt; e < 128 * ch; e += 64) {
-                    const int n = e / ch, c = e % ch;
-                    const bool v = c * 8 < rank && n0 + n < width;
-                    cp_async16_or_zero(w + (c >> 3) * kBlk + swz(n, c & 7), v ? W + (size_t)(n0 + n) * R + c * 8 : W, v);
-                }
-                cp_async_commit();
-                cp_async_wait<0>();
-                if (rank & 7)   // columns past the rank inside a chunk
-                    for (int e = lt; e < 128 * ch; e += 64) {
-                        const int n = e / ch, c = e % ch;
-                        if (c != rank >> 3) continue;
-                        TX *v = reinterpret_cast<TX *>(buf + (w - zs) + (c >> 3) * kBlk + swz(n, c & 7));
-                        for (int j = rank & 7; j < 8; ++j) v[j] = from_f32<TX>(0.f);
-                    }
             }
+            prefetch(i + 2);
+        }
+    } else if (warp == kWorkers / 32 + 2) {
+        // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
+        // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
+        for (int i = 0; fix && i < nts; ++i) {
+            const int s = i % kExpandNS;
+            const bool ok = mbar_wait(&landed[s], (i / kExpandNS) & 1, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            zero_past_rank<kGrad>(buf + (ws - zs) + s * wb, rank, Kp, 128, lane);
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&wfull[s]);
+            if (lane == 0) mbar_arrive(&full[s]);
         }
     } else if (warp == kWorkers / 32) {   // ---- products
         if (lane == 0) {
-            const uint32_t idesc = idesc16<TX>(128, false, kGrad);
+            const uint32_t idesc = idesc16<TX>(128, kGrad, false);
             for (int i = 0; i < nts; ++i) {
-                const int s = i & 1;
-                if (!mbar_wait(&wfull[s], (i >> 1) & 1, p.status)) break;
-                if (i >= 2 && !mbar_wait(&tempty[s], ((i >> 1) & 1) ^ 1, p.status)) break;
+                const int s = i % kExpandNS, b = i & 1;
+                if (!mbar_wait(fix ? &full[s] : &landed[s], (i / kExpandNS) & 1, p.status)) break;
+                if (i >= 2 && !mbar_wait(&tempty[b], ((i >> 1) & 1) ^ 1, p.status)) break;
                 tc_after();
                 const uint32_t w = ws + s * wb;
-                for (int l = 0; l < 2; ++l)
-                    for (int j = 0; j < Kp; j += 16) {
+                for (int l = 0; l < kPieces<TX>; ++l)
+                    for (int j = 0; j < rank; j += 16) {
                         const int at = l * Kp + j;
-                        const uint64_t da = sdesc_k(zs + (at >> 6) * kBlk) + ((at & 63) >> 3);
-                        const uint64_t db = kGrad ? sdesc_mn(w, Kp * 128) + 8 * j : sdesc_k(w + (j >> 6) * kBlk) + ((j & 63) >> 3);
-                        tc_mma16(tmem + s * 128, da, db, idesc, at > 0);
+                        const uint64_t dw = kGrad ? sdesc_mn(w, Kp * 128) + 8 * j : sdesc_k(w + (j >> 6) * kBlk) + ((j & 63) >> 3);
+                        const uint64_t dz = sdesc_k(zs + (at >> 6) * kBlk) + ((at & 63) >> 3);
+                        tc_mma16(tmem + b * 128, dw, dz, idesc, at > 0);
                     }
-                tc_commit(&wempty[s]);
-                tc_commit(&tfull[s]);
+                tc_commit(&empty[s]);
+                tc_commit(&tfull[b]);
             }
         }
-    } else {   // ---- epilogue
+    } else {   // ---- epilogue: tokens [64 half, +64) of columns [32 q4, +32)
         const int q4 = warp & 3, half = warp >> 2;
-        float *sc = reinterpret_cast<float *>(buf + expand_z_bytes(Kp) + 2 * wb + warp * kScratch);
-        const float scale = __ldcg(p.row_scale + (size_t)tile * kTile + q4 * 32 + lane);
-        constexpr int VE = kVec ? 16 / sizeof(TY) : 1;   // elements of a lane's access
-        constexpr int LPR = 32 / VE;                     // lanes of a row
-        constexpr int NI = LPR;                          // accesses of a 32 x 32 block
-        constexpr int RPI = 32 / LPR;                    // rows of an access
-        const int col = (lane % LPR) * VE, rl = lane / LPR;
-        const int passes = 2 * nts;
-        using V = uint4;
-        V pre[kVec ? NI : 1];
-        auto fetch = [&](int ps) {
-            if (!kVec || !in) return;
-            const int n = (nt0 + (ps >> 1)) * 128 + half * 64 + (ps & 1) * 32 + col;
+        constexpr bool kTwo = kPair && sizeof(TY) == 2;   // two tokens per access
+        constexpr int GT = 8, NG = 64 / GT;               // tokens of a group, groups of a block
+        constexpr int kAcc = kTwo ? 4 : 8;                // accesses of a group
+        constexpr int kAhead = kTwo ? 4 : 2;              // groups in flight: 2 KB a warp
+        const int odd = kTwo ? lane & 1 : 0;
+        const int col = q4 * 32 + (kTwo ? lane & ~1 : lane);
+        using V = typename std::conditional<kTwo || sizeof(TY) == 4, uint32_t, uint16_t>::type;
+        V pre[kAhead][kAcc];
+        auto fetch = [&](int g, V (&v)[kAcc]) {   // group g of the run
+            const int n = (nt0 + g / NG) * 128 + col;
 #pragma unroll
-            for (int i = 0; i < NI; ++i) {
-                const int t = s_tok[q4 * 32 + i * RPI + rl];
-                if (t >= 0 && n < width) pre[kVec ? i : 0] = *reinterpret_cast<const V *>(in + t * p.ldy_in + n);
+            for (int a = 0; a < kAcc; ++a) {
+                const int t = s_tok[half * 64 + g % NG * GT + (kTwo ? 2 * a + odd : a)];
+                v[a] = 0;
+                if (in && g < NG * nts && t >= 0 && n < width) v[a] = *reinterpret_cast<const V *>(in + t * p.ldy_in + n);
             }
         };
-        fetch(0);
-        bool ok = true;
-        for (int ps = 0; ps < passes; ++ps) {
-            const int i = ps >> 1, s = i & 1;
-            if (!(ps & 1)) {
-                ok = mbar_wait(&tfull[s], (i >> 1) & 1, p.status);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                tc_after();
-            }
-            const uint32_t t0 = tmem + ((uint32_t)(q4 * 32) << 16) + s * 128 + half * 64 + (ps & 1) * 32;
-            float v[4][8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld8(t0 + 8 * c, v[c]);
-            tc_wait_ld();
-            if (ps & 1) {
-                tc_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&tempty[s]);
-            }
+        for (int g = 0; g < kAhead; ++g) fetch(g, pre[g]);
+        for (int i = 0; i < nts; ++i) {
+            const int b = i & 1, n = (nt0 + i) * 128 + col;
+            const bool ok = mbar_wait(&tfull[b], (i >> 1) & 1, p.status);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_after();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[c][e] *= scale;
-                *reinterpret_cast<float4 *>(sc + lane * 36 + 8 * c) = make_float4(v[c][0], v[c][1], v[c][2], v[c][3]);
-                *reinterpret_cast<float4 *>(sc + lane * 36 + 8 * c + 4) = make_float4(v[c][4], v[c][5], v[c][6], v[c][7]);
-            }
-            __syncwarp();
-            const int n = (nt0 + i) * 128 + half * 64 + (ps & 1) * 32 + col;
-            if (kVec) {
-                V o[NI];
-#pragma unroll
-                for (int k = 0; k < NI; ++k) {
-                    float f[8];
-                    const float *d = sc + (k * RPI + rl) * 36 + col;
-                    *reinterpret_cast<float4 *>(f) = *reinterpret_cast<const float4 *>(d);
-                    if (VE == 8) *reinterpret_cast<float4 *>(f + 4) = *reinterpret_cast<const float4 *>(d + 4);
-                    TY *w = reinterpret_cast<TY *>(&o[k]);
-                    const TY *b = reinterpret_cast<const TY *>(&pre[kVec ? k : 0]);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) w[e] = from_f32<TY>((in ? f32_of(b[e]) : 0.f) + f[e]);
+            for (int g = 0; g < NG; ++g) {
+                const int t0 = half * 64 + g * GT;
+                float v[GT];
+                tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + b * 128 + t0, v);
+                tc_wait_ld();
+                if (g == NG - 1) {
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[b]);
                 }
-                if (ps + 1 < passes) fetch(ps + 1);
 #pragma unroll
-                for (int k = 0; k < NI; ++k) {
-                    const int t = s_tok[q4 * 32 + k * RPI + rl];
-                    if (t >= 0 && n < width) *reinterpret_cast<V *>(y + t * p.ldy + n) = o[k];
+                for (int e = 0; e < GT; e += 4) {
+                    const float4 sc = *reinterpret_cast<const float4 *>(s_scale + t0 + e);
+                    v[e] *= sc.x;
+                    v[e + 1] *= sc.y;
+                    v[e + 2] *= sc.z;
+                    v[e + 3] *= sc.w;
                 }
-            } else {
-                for (int r = 0; r < 32; ++r) {
-                    const int t = s_tok[q4 * 32 + r];
-                    if (t >= 0 && n < width)
-                        y[t * p.ldy + n] = from_f32<TY>((in ? f32_of(in[t * p.ldy_in + n]) : 0.f) + sc[r * 36 + lane]);
+                V o[kAcc];
+#pragma unroll
+                for (int a = 0; a < kAcc; ++a) {
+                    if (kTwo) {   // my token's value of my column, and of my neighbour's
+                        const float mine = odd ? v[(2 * a + 1) % GT] : v[2 * a % GT];
+                        const float theirs = __shfl_xor_sync(0xffffffffu, odd ? v[2 * a % GT] : v[(2 * a + 1) % GT], 1);
+                        o[a] = add_pair<TY>(pre[g % kAhead][a], odd ? theirs : mine, odd ? mine : theirs);
+                    } else if (sizeof(TY) == 4) {
+                        o[a] = add_pair<float>(pre[g % kAhead][a], v[a], 0.f);
+                    } else {
+                        const TY base = *reinterpret_cast<const TY *>(&pre[g % kAhead][a]);
+                        const TY r = from_f32<TY>(f32_of(base) + v[a]);
+                        o[a] = *reinterpret_cast<const V *>(&r);
+                    }
+                }
+                fetch(NG * i + g + kAhead, pre[g % kAhead]);
+#pragma unroll
+                for (int a = 0; a < kAcc; ++a) {
+                    const int t = s_tok[t0 + (kTwo ? 2 * a + odd : a)];
+                    if (t >= 0 && n < width) *reinterpret_cast<V *>(y + t * p.ldy + n) = o[a];
                 }
             }
-            __syncwarp();
         }
         tc_before();
     }
@@ -968,25 +1313,26 @@ int cuda_status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA
 
 int tiles_max(const moe_adapters_desc &d, int T) { return (T + kTile - 1) / kTile + std::min(d.n_adapters + 1, T); }
 int few_splits(const moe_adapters_desc &d) { return (d.in_features + kFewK - 1) / kFewK; }
+int pieces_of(const moe_adapters_desc &d) { return d.dtype == MOE_DTYPE_BF16 ? kPieces<__nv_bfloat16> : kPieces<__half>; }
 int rank_pad(const moe_adapters_desc &d) { return (d.max_rank + 15) / 16 * 16; }
 
 // a call's workspace: the small path's partial sums share the bytes of the other path
 struct AdWs {
-    size_t seg, counts, entry_of, tile_bin, hist, limb, row_scale, zl, dl, dz, amax, total;
+    size_t seg, counts, entry_of, tile_bin, hist, pieces, row_scale, zl, dl, dz, amax, total;
 };
 
 AdWs ad_layout(const moe_adapters_desc &d, int T)
 {
     AdWs w;
     const size_t bins = d.n_adapters + 1, tiles = tiles_max(d, T), rows = tiles * kTile;
-    const size_t pieces = rows * 2 * rank_pad(d) * 2;
+    const size_t pieces = rows * pieces_of(d) * rank_pad(d) * 2;
     size_t o = 0;
     w.seg = o; o = up256(o + (bins + 1) * 4);
     w.counts = o; o = up256(o + bins * 4);
     w.entry_of = o; o = up256(o + rows * 4);
     w.tile_bin = o; o = up256(o + tiles * 4);
     w.hist = o; o = up256(o + ((size_t)T + kSortChunk - 1) / kSortChunk * bins * 4);
-    w.limb = o; o = up256(o + pieces);
+    w.pieces = o; o = up256(o + pieces);
     w.row_scale = o; o = up256(o + rows * 4);
     w.zl = o; o = up256(o + pieces);
     w.dl = o; o = up256(o + pieces);
@@ -1043,15 +1389,53 @@ AdParams ad_params(const moe_adapters *h, const int32_t *adapter_of, int T, void
     p.counts = reinterpret_cast<int32_t *>(at(w.counts));
     p.entry_of = reinterpret_cast<int32_t *>(at(w.entry_of));
     p.tile_bin = reinterpret_cast<int32_t *>(at(w.tile_bin));
-    p.limb = at(w.limb);
+    p.pieces = at(w.pieces);
     p.row_scale = reinterpret_cast<float *>(at(w.row_scale));
     p.zl = at(w.zl);
-    p.dl = d.dtype == MOE_DTYPE_F16 ? at(w.dl) : at(w.limb);   // bf16: dz's pieces serve both products
+    p.dl = d.dtype == MOE_DTYPE_F16 ? at(w.dl) : at(w.pieces);   // bf16: dz's pieces serve both products
     p.dz = reinterpret_cast<float *>(at(w.dz));
     p.amax = reinterpret_cast<unsigned *>(at(w.amax));
     p.z_part = reinterpret_cast<float *>(ws);
     p.splits = few_splits(d);
     return p;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        cudaDriverEntryPointQueryResult q;
+        void *p = nullptr;
+        const bool ok = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                        q == cudaDriverEntryPointSuccess;
+        return ok ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
+    }();
+    return fn;
+}
+
+// 3-D map of a pool's matrices [n][rows][cols] of 16-bit elements, boxes of 64 columns x box
+// rows, 128-byte swizzle
+bool make_pool_map(CUtensorMap *m, const void *base, int cols, int rows, int n, int box_rows)
+{
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)n};
+    const cuuint64_t strides[2] = {(cuuint64_t)cols * 2, (cuuint64_t)cols * 2 * (cuuint64_t)rows};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, unit[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void *>(base), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// 2-D map of rows of pieces, boxes of 64 columns x 64 rows
+bool make_rows_map(CUtensorMap *m, const void *base, int cols, size_t rows)
+{
+    const auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)cols * 2};
+    const cuuint32_t box[2] = {64, 64}, unit[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void *>(base), dims, strides, box, unit,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStream_t s)
@@ -1074,9 +1458,9 @@ cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStr
     return launch_sort(q, s);
 }
 
-template <typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
-                           const AdParams &p)
+template <typename... KArgs, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                           const Args &...args)
 {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -1094,7 +1478,7 @@ cudaError_t launch_cluster(void (*kernel)(Args...), dim3 grid, int threads, size
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // CTAs of a cluster that share `blocks` steps of work so that `units` clusters give every SM
@@ -1106,6 +1490,12 @@ int split_of(long long units, int blocks, int num_sms)
     return S;
 }
 
+// rows of pieces, by position
+bool make_pieces_map(const moe_adapters *h, CUtensorMap *m, const void *base, int T)
+{
+    return make_rows_map(m, base, pieces_of(h->desc) * rank_pad(h->desc), (size_t)tiles_max(h->desc, T) * kTile);
+}
+
 template <typename TX, bool kGrad>
 cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
 {
@@ -1113,32 +1503,45 @@ cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, h->num_sms);
     const size_t ring = (size_t)kShrinkNS * (kBlk + shrink_w_bytes(kGrad, p.R, p.Kp));
     const size_t sums = (size_t)kTile * (p.Kp + 4) * 4;
-    return launch_cluster(shrink_tile_kernel<TX, kGrad>, dim3(tiles * S), kWorkers + 32, 1024 + std::max(ring, sums), S,
-                          s, p);
+    return launch_cluster(shrink_tile_kernel<TX, kGrad>, dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s,
+                          kGrad ? h->map_b64 : h->map_a, p);
 }
 
 template <typename TX>
 cudaError_t run_grad(const moe_adapters *h, const AdParams &p, cudaStream_t s)
 {
+    CUtensorMap dz = {}, z = {};
+    if (p.T && !(make_pieces_map(h, &dz, p.dl, p.T) && make_pieces_map(h, &z, p.zl, p.T))) return cudaErrorInvalidValue;
     const int tiles = (p.K + 127) / 128 + (p.N + 127) / 128, live = std::max(1, std::min(p.n, p.T));
     const int S = split_of((long long)tiles * live, (p.T / live + 63) / 64, h->num_sms);
-    const size_t ring = (size_t)kGradNS * (2 * 8192 + grad_z_bytes(p.Kp));
+    // four stages of 64 tokens where they fit, three for bf16 ranks above 85
+    const size_t stage = 2 * 8192 + grad_z_bytes(kPieces<TX> * p.Kp);
     const size_t sums = (size_t)std::max(128 * (p.Kp + 4), p.Kp * 132) * 4;
-    return launch_cluster(grad_tile_kernel<TX>, dim3(tiles * S, p.n), kWorkers + 32, 1024 + std::max(ring, sums), S, s,
-                          p);
+    const bool four = 4 * stage <= kMaxSmem;
+    return launch_cluster(four ? grad_tile_kernel<TX, 4> : grad_tile_kernel<TX, 3>, dim3(tiles * S, p.n), kTcThreads,
+                          1024 + std::max((four ? 4 : 3) * stage, sums), S, s, dz, z, p);
 }
 
 template <typename TX, typename TY, bool kGrad>
 cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStream_t s)
 {
-    const int tiles = tiles_max(h->desc, p.T), width = kGrad ? p.K : p.N, nts = (width + 127) / 128;
-    const int groups = std::max(1, std::min(nts, 2 * h->num_sms / tiles));
-    const size_t smem = 1024 + expand_z_bytes(p.Kp) + 2 * (size_t)expand_w_bytes(kGrad, p.Kp) + kWorkers / 32 * kScratch;
-    const int es = (int)sizeof(TY);
-    auto wide = [&](const void *q, long long ld) { return !q || (aligned16(q) && ld * es % 16 == 0); };
-    const bool vec = width * es % 16 == 0 && wide(p.y, p.ldy) && wide(p.y_in, p.ldy_in);
-    return launch_cluster(vec ? expand_tile_kernel<TX, TY, kGrad, true> : expand_tile_kernel<TX, TY, kGrad, false>,
-                          dim3(tiles, groups), kExpandThreads, smem, 1, s, p);
+    const int tiles = tiles_max(h->desc, p.T), width = kGrad ? p.K : p.N;
+    const size_t es = sizeof(TY), zb = expand_z_bytes(kPieces<TX> * p.Kp);
+    auto rows16 = [&](const void *q, long long ld) { return !q || (aligned16(q) && ld * es % 16 == 0); };
+    CUtensorMap z;
+    if (width * es % 16 == 0 && rows16(p.y, p.ldy) && rows16(p.y_in, p.ldy_in) && tiles / h->num_sms + 2 <= kMaxRun) {
+        if (!make_pieces_map(h, &z, p.pieces, p.T)) return cudaErrorInvalidValue;
+        const size_t smem = 1024 + zb + 2 * (size_t)expand_w_bytes(kGrad, p.Kp, 128) + kWorkers * kPitch * 4;
+        return launch_cluster(expand_tile_kernel<TX, TY, kGrad>, dim3(h->num_sms), kExpandThreads, smem, 1, s,
+                              kGrad ? h->map_a : h->map_b, z, p);
+    }
+    const int groups = std::max(1, std::min((width + 127) / 128, 2 * h->num_sms / tiles));
+    const size_t smem = 1024 + zb + kExpandNS * (size_t)expand_w_bytes(kGrad, p.Kp, 128);
+    auto pairs = [&](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0; };
+    const bool pair = width % 2 == 0 && pairs(p.y, p.ldy) && (!p.y_in || pairs(p.y_in, p.ldy_in));
+    const bool two = sizeof(TY) == 2 && pair;   // (fp32 has no pairs)
+    return launch_cluster(two ? expand_any_kernel<TX, TY, kGrad, sizeof(TY) == 2> : expand_any_kernel<TX, TY, kGrad, false>,
+                          dim3(tiles, groups), kExpandThreads, smem, 1, s, kGrad ? h->map_a : h->map_b, p);
 }
 
 template <typename TX, bool kGrad>
@@ -1229,6 +1632,9 @@ int moe_adapters_create(const moe_adapters_desc *desc, const moe_adapters_weight
     h->w = w;
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
+        !make_pool_map(&h->map_a, w.a, d.in_features, d.max_rank, d.n_adapters, rank_pad(d)) ||
+        !make_pool_map(&h->map_b, w.b, d.max_rank, d.out_features, d.n_adapters, 128) ||
+        !make_pool_map(&h->map_b64, w.b, d.max_rank, d.out_features, d.n_adapters, 64) ||
         cudaMalloc(&h->d_status, 256) != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;
