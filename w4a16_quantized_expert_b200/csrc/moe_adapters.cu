@@ -535,6 +535,7 @@ __global__ void __launch_bounds__(kTcThreads)
         const int per = kTile / S;
         const float scaling = kGrad ? __ldcg(p.scaling + bin) : 1.f;
         const float apply_scale = kGrad ? 1.f : __ldcg(p.scaling + bin);
+#pragma unroll 2
         for (int r = q * per + warp; r < (q + 1) * per; r += kWorkers / 32) {
             const int tok = s_tok[r];
             const size_t pos = (size_t)tile * kTile + r;
@@ -545,12 +546,11 @@ __global__ void __launch_bounds__(kTcThreads)
                 v[i] = 0.f;
                 if (col < Kp) {
                     const uint32_t at = sbuf + (uint32_t)(r * pitch + col) * 4;
-                    if (S > 1) {
-#pragma unroll 8
-                        for (int c = 0; c < S; ++c) v[i] += ld_cluster(peer_addr(at, c));
-                    } else {
-                        v[i] = reinterpret_cast<float *>(buf)[r * pitch + col];
-                    }
+                    float part[kMaxSplit];
+#pragma unroll
+                    for (int c = 0; c < kMaxSplit; ++c) part[c] = c < S ? ld_cluster(peer_addr(at, c)) : 0.f;
+#pragma unroll
+                    for (int c = 0; c < kMaxSplit; ++c) v[i] += part[c];
                     if (col >= rank || tok < 0) v[i] = 0.f;   // (what lies past the rank is not used)
                     v[i] *= scaling;
                 }
@@ -680,10 +680,12 @@ __global__ void __launch_bounds__(kTcThreads)
         const int cx = tid & 15, rx = tid >> 4;   // 16-byte chunk of a row, first of four rows
         const bool in_x = cx * 8 < cols;
         const TX *Xc = X + c0 + cx * 8;
-        const int32_t *ids = p.entry_of + pos0 + q * 64 + rx;
-        int t[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) t[u] = steps > 0 ? __ldcg(ids + 16 * u) : -1;
+        // the warp's eight tokens of four steps, a lane each, loaded four steps ahead
+        auto tokens = [&](int i) {
+            const int step = i + (lane >> 3), row = 16 * ((lane >> 1) & 3) + (warp << 1) + (lane & 1);
+            return step < steps ? __ldcg(p.entry_of + pos0 + (size_t)(q + step * S) * 64 + row) : -1;
+        };
+        int ids = tokens(0), next = tokens(4);
         ring_load<NS>(ring, steps, p.status, [&](int s, int i) {
             const uint32_t xs = sbuf + s * stage + (cx >> 3) * 8192, zs = sbuf + s * stage + 2 * 8192;
             if (tid == 0) {
@@ -691,14 +693,16 @@ __global__ void __launch_bounds__(kTcThreads)
                 for (int c = 0; c * 64 < ZC; ++c)
                     tma_box2(zs + c * 8192, mz, &ring.full[s], c * 64, (int)pos0 + (q + i * S) * 64);
             }
+            if (i && (i & 3) == 0) {
+                ids = next;
+                next = tokens(i + 4);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const bool in = t[u] >= 0 && in_x;
-                cp_async16_or_zero(xs + swz(rx + 16 * u, cx & 7), in ? Xc + t[u] * ld : X, in);
+                const int t = __shfl_sync(0xffffffffu, ids, (i & 3) * 8 + 2 * u + (lane >> 4));
+                const bool in = t >= 0 && in_x;
+                cp_async16_or_zero(xs + swz(rx + 16 * u, cx & 7), in ? Xc + t * ld : X, in);
             }
-            if (i + 1 < steps)   // the next step's tokens, a step ahead
-#pragma unroll
-                for (int u = 0; u < 4; ++u) t[u] = __ldcg(ids + (size_t)(i + 1) * S * 64 + 16 * u);
         });
         if (steps > 0) mbar_wait(&ring.done, 0, p.status);
         __syncwarp();
@@ -754,14 +758,18 @@ __global__ void __launch_bounds__(kTcThreads)
             if (!is_b && c4 >= cols) continue;                // (K is a multiple of 8)
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
             const uint32_t at = sbuf + (uint32_t)(row * pitch + c4) * 4;
-#pragma unroll 8
-            for (int c = 0; c < S; ++c) {
-                const float4 o = S > 1 ? ld_cluster4(peer_addr(at, c)) : *reinterpret_cast<float4 *>(P + row * pitch + c4);
-                v.x += o.x;
-                v.y += o.y;
-                v.z += o.z;
-                v.w += o.w;
-            }
+            float4 part[kMaxSplit];
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c)
+                if (c < S) part[c] = ld_cluster4(peer_addr(at, c));
+#pragma unroll
+            for (int c = 0; c < kMaxSplit; ++c)
+                if (c < S) {
+                    v.x += part[c].x;
+                    v.y += part[c].y;
+                    v.z += part[c].z;
+                    v.w += part[c].w;
+                }
             float *f = &v.x;
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = (is_b ? c4 + e : row) < rank ? f[e] * scale : 0.f;
@@ -782,19 +790,26 @@ __global__ void __launch_bounds__(kTcThreads)
 }
 
 // y[t][n] = y_in[t][n] + sum_j z[t][j] B[n][j] (kGrad: dx = dx_in + dz A), whose rows are 16-byte
-// aligned.  A persistent CTA per SM takes a run of (tile, block of 128 columns) items.
+// aligned.  A persistent CTA per SM takes a run of (tile, 256 bytes of columns) items.
 // Operands: z's pieces [128 tokens][pieces x Kp] K-major, loaded once per tile; B [columns]
-// [ranks] K-major, or A [ranks][columns] MN-major, two stages; both by TMA; D in TMEM, double
-// buffered.  Eight epilogue warps (32 tokens x 64 columns each) turn D's rows (a TMEM lane is
-// a token) into coalesced rows through shared memory, 32 columns at a time, and add y_in,
-// whose loads run 64 KB ahead per SM.  Bound by reading y_in and writing y.  Measured for
+// [ranks] K-major, or A [ranks][columns] MN-major, in a ring; both by TMA; D in TMEM, double
+// buffered.  Eight epilogue warps (32 tokens x 128 bytes each) turn D's rows (a TMEM lane is
+// a token) into coalesced rows through shared memory and add y_in, whose loads run 64 KB
+// ahead per SM.  Bound by reading y_in and writing y.  Measured for
 // 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): EXPAND_US us;
 // a lane per token straight to memory 67 us and a lane per column 44 us (the load/store
 // unit), TMA row gathers and scatters 62 us (about 75 cycles per four rows).
 constexpr int kExpandThreads = kWorkers + 96;   // epilogue, MMA, TMA, fix warps
-constexpr int kExpandNS = 3;
+constexpr int kExpandNS = 4;                    // weight stages at most
+constexpr int kAnyNS = 3;
 constexpr int kMaxRun = 16;                     // tiles that a CTA's run may touch
-constexpr int kPitch = 36;                      // floats of a row of an epilogue warp's block
+
+// pieces that an output's type can tell apart: two carry 16 bits or more of z
+template <typename TX, typename TY>
+__host__ __device__ constexpr int use_pieces()
+{
+    return sizeof(TY) == 2 ? 2 : kPieces<TX>;
+}
 
 __host__ __device__ inline int expand_z_bytes(int cols) { return (cols + 63) / 64 * kBlk; }
 // bytes of a weight stage of n columns of the output
@@ -855,10 +870,10 @@ __device__ __forceinline__ uint32_t add_pair<float>(uint32_t base, float a, floa
 template <typename TX, typename TY, bool kGrad>
 __global__ void __launch_bounds__(kExpandThreads, 1)
     expand_tile_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_z,
-                       const AdParams p)
+                       const AdParams p, const int ns)
 {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t zfull, zempty, wland[2], wfull[2], wempty[2], tfull[2], tempty[2];
+    __shared__ uint64_t zfull, zempty, wland[kExpandNS], wfull[kExpandNS], wempty[kExpandNS], tfull[2], tempty[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_bin[kMaxRun], s_rank[kMaxRun];
     __shared__ int s_tok[kMaxRun * kTile];
@@ -868,10 +883,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     if (tid == 0) {
         mbar_init(&zfull, 1);
         mbar_init(&zempty, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < ns; ++i) {
             mbar_init(&wland[i], 1);
             mbar_init(&wfull[i], 1);
             mbar_init(&wempty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], kWorkers / 32);
         }
@@ -880,9 +897,11 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     pdl_wait();
     pdl_trigger();
     if (warp == kMmaWarp) tc_alloc(&s_tmem, 256);
-    const int Kp = p.Kp, ZC = kPieces<TX> * Kp, width = kGrad ? p.K : p.N;
-    const int zb = expand_z_bytes(ZC), wb = expand_w_bytes(kGrad, Kp, 128);
-    const int nt_all = (width + 127) / 128;
+    constexpr int NW = 256 / sizeof(TY), NB = 128 / sizeof(TY);   // columns of an item, of a warp
+    constexpr int kUse = use_pieces<TX, TY>();
+    const int Kp = p.Kp, width = kGrad ? p.K : p.N;
+    const int zb = expand_z_bytes(kUse * Kp), wb = expand_w_bytes(kGrad, Kp, NW);
+    const int nt_all = (width + NW - 1) / NW;
     const long long items = (long long)(__ldcg(p.seg + p.n + 1) / kTile) * nt_all;
     const int lo = (int)(items * blockIdx.x / gridDim.x), hi = (int)(items * (blockIdx.x + 1) / gridDim.x);
     // the run's tiles: adapters, ranks, tokens, scales
@@ -901,13 +920,27 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     const uint32_t zs = smem_u32(buf), ws = zs + zb, tmem = s_tmem;
     const TY *in = static_cast<const TY *>(p.y_in);
     TY *y = static_cast<TY *>(p.y);
-    // every role walks the same items; j counts the ones that have a product, zc their tiles
-    int cur = -1, j = 0, zc = 0;
+    // every role walks the same items; j counts the ones that have a product (stage s of the
+    // ring, in its turn `ph`), zc their tiles
+    int cur = -1, j = 0, zc = 0, s = 0, ph = 0;
+    auto advance = [&] {
+        ++j;
+        if (++s == ns) s = 0, ph ^= 1;
+    };
     if (warp == kTmaWarp) {   // ---- copies of the operands
         if (lane == 0)
             for (int it = lo; it < hi; ++it) {
-                const int lt = it / nt_all - tile0, n0 = it % nt_all * 128, s = j & 1;
+                const int lt = it / nt_all - tile0, n0 = it % nt_all * NW;
                 if (!s_rank[lt]) continue;
+                if (j >= ns && !mbar_wait(&wempty[s], ph ^ 1, p.status)) break;
+                const uint32_t w = ws + s * wb;
+                mbar_arrive_expect_tx(&wland[s], wb);
+                if (kGrad) {
+                    for (int b = 0; b < NW / 64; ++b) tma_box(w + b * Kp * 128, &map_w, &wland[s], n0 + b * 64, 0, s_bin[lt]);
+                } else {
+                    tma_box(w, &map_w, &wland[s], 0, n0, s_bin[lt]);
+                    if (Kp > 64) tma_box(w + NW * 128, &map_w, &wland[s], 64, n0, s_bin[lt]);
+                }
                 if (lt != cur) {
                     cur = lt;
                     if (zc && !mbar_wait(&zempty, (zc - 1) & 1, p.status)) break;
@@ -917,39 +950,30 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                             tma_box2(zs + b * kBlk + r * 128, &map_z, &zfull, b * 64, (tile0 + lt) * kTile + r);
                     ++zc;
                 }
-                if (j >= 2 && !mbar_wait(&wempty[s], ((j >> 1) & 1) ^ 1, p.status)) break;
-                const uint32_t w = ws + s * wb;
-                mbar_arrive_expect_tx(&wland[s], wb);
-                if (kGrad) {
-                    tma_box(w, &map_w, &wland[s], n0, 0, s_bin[lt]);
-                    tma_box(w + Kp * 128, &map_w, &wland[s], n0 + 64, 0, s_bin[lt]);
-                } else {
-                    tma_box(w, &map_w, &wland[s], 0, n0, s_bin[lt]);
-                    if (Kp > 64) tma_box(w + kBlk, &map_w, &wland[s], 64, n0, s_bin[lt]);
-                }
-                ++j;
+                advance();
             }
     } else if (warp == kTmaWarp + 1) {
         // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
         // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
         for (int it = lo; it < hi; ++it) {
-            const int rank = s_rank[it / nt_all - tile0], s = j & 1;
+            const int rank = s_rank[it / nt_all - tile0];
             if (!rank) continue;
-            const bool ok = mbar_wait(&wland[s], (j >> 1) & 1, p.status);
+            const bool ok = mbar_wait(&wland[s], ph, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (rank & 15) {
-                zero_past_rank<kGrad>(buf + zb + s * wb, rank, Kp, 128, lane);
+                zero_past_rank<kGrad>(buf + zb + s * wb, rank, Kp, NW, lane);
                 fence_async_smem();
                 __syncwarp();
             }
             if (lane == 0) mbar_arrive(&wfull[s]);
-            ++j;
+            advance();
         }
     } else if (warp == kMmaWarp) {   // ---- products
         if (lane == 0) {
-            const uint32_t idesc = idesc16<TX>(128, false, kGrad);
+            const uint32_t idesc = idesc16<TX>(NW, false, kGrad);
+            const uint64_t dz0 = sdesc_k(zs), dw0 = kGrad ? sdesc_mn(ws, Kp * 128) : sdesc_k(ws);
             for (int it = lo; it < hi; ++it) {
-                const int lt = it / nt_all - tile0, rank = s_rank[lt], s = j & 1;
+                const int lt = it / nt_all - tile0, rank = s_rank[lt], b = j & 1;
                 if (!rank) continue;
                 if (lt != cur) {
                     cur = lt;
@@ -957,106 +981,103 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                     if (!mbar_wait(&zfull, zc & 1, p.status)) break;
                     ++zc;
                 }
-                if (!mbar_wait(&wfull[s], (j >> 1) & 1, p.status)) break;
-                if (j >= 2 && !mbar_wait(&tempty[s], ((j >> 1) & 1) ^ 1, p.status)) break;
+                if (!mbar_wait(&wfull[s], ph, p.status)) break;
+                if (j >= 2 && !mbar_wait(&tempty[b], ((j >> 1) & 1) ^ 1, p.status)) break;
                 tc_after();
-                const uint32_t w = ws + s * wb;
-                for (int l = 0; l < kPieces<TX>; ++l)
-                    for (int k = 0; k < rank; k += 16) {
-                        const int at = l * Kp + k;
-                        const uint64_t dz = sdesc_k(zs + (at >> 6) * kBlk) + ((at & 63) >> 3);
-                        const uint64_t dw = kGrad ? sdesc_mn(w, Kp * 128) + 8 * k : sdesc_k(w + (k >> 6) * kBlk) + ((k & 63) >> 3);
-                        tc_mma16(tmem + s * 128, dz, dw, idesc, at > 0);
+                const uint64_t dw = dw0 + ((s * wb) >> 4);
+                const int steps = (rank + 15) >> 4;
+                for (int l = 0; l < kUse; ++l)
+                    for (int k = 0; k < steps; ++k) {   // (a 64-column block holds four steps)
+                        const int at = l * (Kp >> 4) + k;
+                        tc_mma16(tmem + b * 128, dz0 + (at >> 2) * (kBlk >> 4) + (at & 3) * 2,
+                                 dw + (kGrad ? 128 * k : (k >> 2) * (NW * 8) + (k & 3) * 2), idesc, at > 0);
                     }
                 tc_commit(&wempty[s]);
-                tc_commit(&tfull[s]);
-                ++j;
+                tc_commit(&tfull[b]);
+                advance();
             }
         }
-    } else {   // ---- epilogue: tokens [32 q4, +32), columns [64 half, +64)
+    } else {   // ---- epilogue: tokens [32 q4, +32), 128 bytes of columns
         const int q4 = warp & 3, half = warp >> 2;
-        float *sc = reinterpret_cast<float *>(buf + zb + 2 * wb) + warp * 32 * kPitch;
-        constexpr int CE = 16 / sizeof(TY);           // elements of a 16-byte access
-        constexpr int LPR = 32 / CE, NA = LPR;        // lanes of a row, accesses of a 32 x 32 pass
-        constexpr int kItems = sizeof(TY) == 2 ? 2 : 1;   // items whose y_in is in flight: 8 KB a warp
-        const int rl = lane / LPR, cl = lane % LPR * CE;
-        uint4 pre[kItems][2][NA];
-        auto row_token = [&](int it, int a) { return s_tok[(it / nt_all - tile0) * kTile + q4 * 32 + a * (32 / LPR) + rl]; };
-        auto fetch = [&](int it, int ps, uint4 (&v)[NA]) {
-            const int n = it % nt_all * 128 + half * 64 + ps * 32 + cl;
+        constexpr int kPitch = NB + 4;                // floats of a row of the warp's block
+        float *sc = reinterpret_cast<float *>(buf + zb + ns * wb) + warp * 32 * kPitch;
+        constexpr int CE = 16 / sizeof(TY), NA = 8;   // a lane's 16 bytes, 8 lanes a row: 8 accesses of 4 rows
+        constexpr int kItems = 2;                     // items whose y_in is in flight: 8 KB a warp
+        const int rl = lane >> 3, cl = half * NB + (lane & 7) * CE;
+        uint4 pre[kItems][NA];
+        auto fetch = [&](int it, uint4 (&v)[NA]) {
+            const int n = it % nt_all * NW + cl;
             if (!in || it >= hi || n >= width) return;
+            const int *tok = s_tok + (it / nt_all - tile0) * kTile + q4 * 32 + rl;
 #pragma unroll
             for (int a = 0; a < NA; ++a) {
-                const int t = row_token(it, a);
+                const int t = tok[4 * a];
                 if (t >= 0) v[a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
             }
         };
 #pragma unroll
-        for (int u = 0; u < kItems; ++u)
+        for (int u = 0; u < kItems; ++u) {
 #pragma unroll
-            for (int ps = 0; ps < 2; ++ps) {
-#pragma unroll
-                for (int a = 0; a < NA; ++a) pre[u][ps][a] = make_uint4(0u, 0u, 0u, 0u);
-                fetch(lo + u, ps, pre[u][ps]);
-            }
+            for (int a = 0; a < NA; ++a) pre[u][a] = make_uint4(0u, 0u, 0u, 0u);
+            fetch(lo + u, pre[u]);
+        }
         bool ok = true;
         for (int it0 = lo; it0 < hi && ok; it0 += kItems)
 #pragma unroll
             for (int u = 0; u < kItems; ++u) {
                 const int it = it0 + u;
                 if (it >= hi || !ok) continue;
-                const int lt = it / nt_all - tile0, s = j & 1;
+                const int lt = it / nt_all - tile0, b = j & 1, n = it % nt_all * NW + cl;
                 const bool product = s_rank[lt] > 0;
+                const int *tok = s_tok + lt * kTile + q4 * 32 + rl;
+                uint4 o[NA];
                 if (product) {
-                    ok = mbar_wait(&tfull[s], (j >> 1) & 1, p.status);
+                    ok = mbar_wait(&tfull[b], (j >> 1) & 1, p.status);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) continue;
                     tc_after();
-                    ++j;
-                }
-                const float scale = s_scale[lt * kTile + q4 * 32 + lane];
+                    const float scale = s_scale[lt * kTile + q4 * 32 + lane];
 #pragma unroll
-                for (int ps = 0; ps < 2; ++ps) {
-                    const int n = it % nt_all * 128 + half * 64 + ps * 32 + cl;
-                    uint4 o[NA];
-                    if (product) {
+                    for (int h = 0; h < NB; h += 32) {
                         float v[32];
-                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + s * 128 + half * 64 + ps * 32, v);
+                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + b * 128 + half * NB + h, v);
                         tc_wait_ld();
-                        if (ps == 1) {
-                            tc_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(&tempty[s]);
-                        }
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(sc + lane * kPitch + e) =
+                            *reinterpret_cast<float4 *>(sc + lane * kPitch + h + e) =
                                 make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
-                        __syncwarp();
-#pragma unroll
-                        for (int a = 0; a < NA; ++a) {
-                            const float *d = sc + (a * (32 / LPR) + rl) * kPitch + cl;
-                            uint32_t *f = &o[a].x;
-                            const uint32_t *base = &pre[u][ps][a].x;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (sizeof(TY) == 4) f[e] = add_pair<TY>(base[e], d[e], 0.f);
-                                else f[e] = add_pair<TY>(base[e], d[2 * e], d[2 * e + 1]);
-                            }
-                        }
-                        __syncwarp();
-                    } else {   // no product: the base's bits
-#pragma unroll
-                        for (int a = 0; a < NA; ++a) o[a] = pre[u][ps][a];
                     }
-                    fetch(it + kItems, ps, pre[u][ps]);
-                    if ((product || in != y) && n < width)
+                    tc_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[b]);
+                    ++j;
 #pragma unroll
-                        for (int a = 0; a < NA; ++a) {
-                            const int t = row_token(it, a);
-                            if (t >= 0) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o[a];
+                    for (int a = 0; a < NA; ++a) {
+                        float d[CE];
+#pragma unroll
+                        for (int e = 0; e < CE; e += 4)
+                            *reinterpret_cast<float4 *>(d + e) =
+                                *reinterpret_cast<const float4 *>(sc + (4 * a + rl) * kPitch + (lane & 7) * CE + e);
+                        uint32_t *f = &o[a].x;
+                        const uint32_t *base = &pre[u][a].x;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if (sizeof(TY) == 4) f[e] = add_pair<TY>(base[e], d[e % CE], 0.f);
+                            else f[e] = add_pair<TY>(base[e], d[2 * e % CE], d[(2 * e + 1) % CE]);
                         }
+                    }
+                    __syncwarp();
+                } else {   // no product: the base's bits
+#pragma unroll
+                    for (int a = 0; a < NA; ++a) o[a] = pre[u][a];
                 }
+                fetch(it + kItems, pre[u]);
+                if ((product || in != y) && n < width)
+#pragma unroll
+                    for (int a = 0; a < NA; ++a) {
+                        const int t = tok[4 * a];
+                        if (t >= 0) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o[a];
+                    }
             }
         tc_before();
     }
@@ -1100,7 +1121,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2)
     expand_any_kernel(const __grid_constant__ CUtensorMap map, const AdParams p)
 {
     extern __shared__ unsigned char raw[];
-    __shared__ uint64_t landed[kExpandNS], full[kExpandNS], empty[kExpandNS], tfull[2], tempty[2];
+    __shared__ uint64_t landed[kAnyNS], full[kAnyNS], empty[kAnyNS], tfull[2], tempty[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_tok[kTile];
     __shared__ __align__(16) float s_scale[kTile];
@@ -1132,7 +1153,7 @@ __global__ void __launch_bounds__(kExpandThreads, 2)
     const uint32_t zs = smem_u32(buf), ws = zs + expand_z_bytes(ZC), wb = expand_w_bytes(kGrad, Kp, 128);
     const bool fix = rank & 15;
     if (tid == 0) {
-        for (int i = 0; i < kExpandNS; ++i) {
+        for (int i = 0; i < kAnyNS; ++i) {
             mbar_init(&landed[i], 1);
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
@@ -1178,10 +1199,10 @@ __global__ void __launch_bounds__(kExpandThreads, 2)
         prefetch(0);
         prefetch(1);
         for (int i = 0; i < nts; ++i) {
-            const int s = i % kExpandNS, n0 = (nt0 + i) * 128;
+            const int s = i % kAnyNS, n0 = (nt0 + i) * 128;
             const uint32_t w = ws + s * wb;
             bool ok = true;
-            if (i >= kExpandNS) ok = mbar_wait(&empty[s], ((i / kExpandNS) & 1) ^ 1, p.status);
+            if (i >= kAnyNS) ok = mbar_wait(&empty[s], ((i / kAnyNS) & 1) ^ 1, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&landed[s], wb);
@@ -1199,8 +1220,8 @@ __global__ void __launch_bounds__(kExpandThreads, 2)
         // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
         // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
         for (int i = 0; fix && i < nts; ++i) {
-            const int s = i % kExpandNS;
-            const bool ok = mbar_wait(&landed[s], (i / kExpandNS) & 1, p.status);
+            const int s = i % kAnyNS;
+            const bool ok = mbar_wait(&landed[s], (i / kAnyNS) & 1, p.status);
             if (!__all_sync(0xffffffffu, ok)) break;
             zero_past_rank<kGrad>(buf + (ws - zs) + s * wb, rank, Kp, 128, lane);
             fence_async_smem();
@@ -1211,12 +1232,12 @@ __global__ void __launch_bounds__(kExpandThreads, 2)
         if (lane == 0) {
             const uint32_t idesc = idesc16<TX>(128, kGrad, false);
             for (int i = 0; i < nts; ++i) {
-                const int s = i % kExpandNS, b = i & 1;
-                if (!mbar_wait(fix ? &full[s] : &landed[s], (i / kExpandNS) & 1, p.status)) break;
+                const int s = i % kAnyNS, b = i & 1;
+                if (!mbar_wait(fix ? &full[s] : &landed[s], (i / kAnyNS) & 1, p.status)) break;
                 if (i >= 2 && !mbar_wait(&tempty[b], ((i >> 1) & 1) ^ 1, p.status)) break;
                 tc_after();
                 const uint32_t w = ws + s * wb;
-                for (int l = 0; l < kPieces<TX>; ++l)
+                for (int l = 0; l < use_pieces<TX, TY>(); ++l)   // (as above: the same bits)
                     for (int j = 0; j < rank; j += 16) {
                         const int at = l * Kp + j;
                         const uint64_t dw = kGrad ? sdesc_mn(w, Kp * 128) + 8 * j : sdesc_k(w + (j >> 6) * kBlk) + ((j & 63) >> 3);
@@ -1531,12 +1552,14 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
     CUtensorMap z;
     if (width * es % 16 == 0 && rows16(p.y, p.ldy) && rows16(p.y_in, p.ldy_in) && tiles / h->num_sms + 2 <= kMaxRun) {
         if (!make_pieces_map(h, &z, p.pieces, p.T)) return cudaErrorInvalidValue;
-        const size_t smem = 1024 + zb + 2 * (size_t)expand_w_bytes(kGrad, p.Kp, 128) + kWorkers * kPitch * 4;
-        return launch_cluster(expand_tile_kernel<TX, TY, kGrad>, dim3(h->num_sms), kExpandThreads, smem, 1, s,
-                              kGrad ? h->map_a : h->map_b, z, p);
+        const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kWorkers * (128 / es + 4) * 4;
+        const size_t fixed = 1024 + expand_z_bytes(use_pieces<TX, TY>() * p.Kp) + scratch;
+        const int ns = (int)std::min<size_t>(kExpandNS, (kMaxSmem - 16 * 1024 - fixed) / wb);   // (16 KB: the run's tiles)
+        return launch_cluster(expand_tile_kernel<TX, TY, kGrad>, dim3(h->num_sms), kExpandThreads, fixed + ns * wb, 1, s,
+                              kGrad ? h->map_a : es == 4 ? h->map_b64 : h->map_b, z, p, ns);
     }
     const int groups = std::max(1, std::min((width + 127) / 128, 2 * h->num_sms / tiles));
-    const size_t smem = 1024 + zb + kExpandNS * (size_t)expand_w_bytes(kGrad, p.Kp, 128);
+    const size_t smem = 1024 + zb + kAnyNS * (size_t)expand_w_bytes(kGrad, p.Kp, 128);
     auto pairs = [&](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0; };
     const bool pair = width % 2 == 0 && pairs(p.y, p.ldy) && (!p.y_in || pairs(p.y_in, p.ldy_in));
     const bool two = sizeof(TY) == 2 && pair;   // (fp32 has no pairs)
