@@ -366,18 +366,19 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
 // Ring of shared-memory stages between the load warps and the thread that issues the MMAs.
 // A load thread copies its share of a stage's rows with cp.async (a tile's tokens lie
 // anywhere; row gathers by TMA were slower: 26 against 21 us for the shrink of 4096 tokens of
-// 6144) and reports it kLag steps later, when the copies have landed, with one arrival per
-// warp; the weights' boxes come by TMA and add one arrival.
+// 6144) and leaves an arrival behind that follows the copies; the weights' boxes come by TMA
+// and add one arrival.  The MMA thread makes the copies visible to the tensor core.
 template <int NS>
 struct Ring {
     uint64_t full[NS], empty[NS], done;
-    __device__ void init(int arrivals)
+    __device__ void init()
     {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], arrivals);
+            mbar_init(&full[i], kWorkers + 1);
             mbar_init(&empty[i], 1);
         }
         mbar_init(&done, 1);
+        fence_mbar_init();
     }
 };
 
@@ -385,23 +386,13 @@ struct Ring {
 template <int NS, typename F>
 __device__ __forceinline__ void ring_load(Ring<NS> &r, int steps, int *status, F &&copy)
 {
-    constexpr int kLag = NS - 1;
-    for (int i = 0; i < steps + kLag; ++i) {
-        if (i < steps) {
-            bool ok = true;
-            if (i >= NS) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
-            if (!__all_sync(0xffffffffu, ok)) break;
-            copy(i % NS, i);
-        }
-        cp_async_commit();
-        if (i >= kLag) {
-            cp_async_wait<kLag>();
-            fence_async_smem();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(&r.full[(i - kLag) % NS]);
-        }
+    for (int i = 0; i < steps; ++i) {
+        bool ok = true;
+        if (i >= NS) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        copy(i % NS, i);
+        cp_async_arrive(&r.full[i % NS]);
     }
-    cp_async_wait<0>();
 }
 
 // Issue loop of the MMA thread: mma(stage, i) issues the MMAs of step i.
@@ -410,6 +401,7 @@ __device__ __forceinline__ void ring_mma(Ring<NS> &r, int steps, int *status, F 
 {
     for (int i = 0; i < steps; ++i) {
         if (!mbar_wait(&r.full[i % NS], (i / NS) & 1, status)) return;
+        fence_async_smem();
         tc_after();
         mma(i % NS, i);
         tc_commit(&r.empty[i % NS]);
@@ -459,8 +451,7 @@ __global__ void __launch_bounds__(kTcThreads)
     }
     if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);
     if (tid == 0) {
-        ring.init(kWorkers / 32 + 1);
-        fence_mbar_init();
+        ring.init();
     }
     if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(Kp));
     tc_before();
@@ -502,6 +493,7 @@ __global__ void __launch_bounds__(kTcThreads)
                 cp_async16_or_zero(xs + swz(r0 + 32 * u, c), live[u] && in ? px[u] + k0 : X, live[u] && in);
         });
         mbar_wait(&ring.done, 0, p.status);
+        cp_async_wait<0>();
         __syncwarp();
         tc_after();
         float *P = reinterpret_cast<float *>(buf);
@@ -661,8 +653,7 @@ __global__ void __launch_bounds__(kTcThreads)
     }
     const size_t pos0 = (size_t)__ldcg(p.seg + a);
     if (tid == 0) {
-        ring.init(kWorkers / 32 + 1);
-        fence_mbar_init();
+        ring.init();
     }
     if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(ZC));
     tc_before();
@@ -705,6 +696,7 @@ __global__ void __launch_bounds__(kTcThreads)
             }
         });
         if (steps > 0) mbar_wait(&ring.done, 0, p.status);
+        cp_async_wait<0>();
         __syncwarp();
         tc_after();
         const int c = (warp & 3) * 32 + lane, half = warp >> 2;
@@ -1005,21 +997,25 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         constexpr int kItems = 2;                     // items whose y_in is in flight: 8 KB a warp
         const int rl = lane >> 3, cl = half * NB + (lane & 7) * CE;
         uint4 pre[kItems][NA];
-        auto fetch = [&](int it, uint4 (&v)[NA]) {
-            const int n = it % nt_all * NW + cl;
-            if (!in || it >= hi || n >= width) return;
-            const int *tok = s_tok + (it / nt_all - tile0) * kTile + q4 * 32 + rl;
+        // the next item to load and the next to finish: tile of the run, block of columns
+        int f_it = lo, f_lt = 0, f_nt = lo - tile0 * nt_all, lt = f_lt, nt = f_nt;
+        auto fetch = [&](uint4 (&v)[NA]) {
+            const int n = f_nt * NW + cl;
+            const int *tok = s_tok + f_lt * kTile + q4 * 32 + rl;
+            if (in && f_it < hi && n < width)
 #pragma unroll
-            for (int a = 0; a < NA; ++a) {
-                const int t = tok[4 * a];
-                if (t >= 0) v[a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
-            }
+                for (int a = 0; a < NA; ++a) {
+                    const int t = tok[4 * a];
+                    if (t >= 0) v[a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
+                }
+            ++f_it;
+            if (++f_nt == nt_all) f_nt = 0, ++f_lt;
         };
 #pragma unroll
         for (int u = 0; u < kItems; ++u) {
 #pragma unroll
             for (int a = 0; a < NA; ++a) pre[u][a] = make_uint4(0u, 0u, 0u, 0u);
-            fetch(lo + u, pre[u]);
+            fetch(pre[u]);
         }
         bool ok = true;
         for (int it0 = lo; it0 < hi && ok; it0 += kItems)
@@ -1027,7 +1023,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             for (int u = 0; u < kItems; ++u) {
                 const int it = it0 + u;
                 if (it >= hi || !ok) continue;
-                const int lt = it / nt_all - tile0, b = j & 1, n = it % nt_all * NW + cl;
+                const int b = j & 1, n = nt * NW + cl;
                 const bool product = s_rank[lt] > 0;
                 const int *tok = s_tok + lt * kTile + q4 * 32 + rl;
                 uint4 o[NA];
@@ -1054,10 +1050,16 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 #pragma unroll
                     for (int a = 0; a < NA; ++a) {
                         float d[CE];
-#pragma unroll
-                        for (int e = 0; e < CE; e += 4)
-                            *reinterpret_cast<float4 *>(d + e) =
-                                *reinterpret_cast<const float4 *>(sc + (4 * a + rl) * kPitch + (lane & 7) * CE + e);
+                        const float *src = sc + (4 * a + rl) * kPitch + (lane & 7) * CE;
+                        if (CE == 8) {   // (lanes 4 .. 7 of a row take their halves in turn: no bank twice)
+                            const int h = lane & 4;
+                            const float4 x = *reinterpret_cast<const float4 *>(src + h);
+                            const float4 w = *reinterpret_cast<const float4 *>(src + (h ^ 4));
+                            *reinterpret_cast<float4 *>(d) = h ? w : x;
+                            *reinterpret_cast<float4 *>(d + CE - 4) = h ? x : w;
+                        } else {
+                            *reinterpret_cast<float4 *>(d) = *reinterpret_cast<const float4 *>(src);
+                        }
                         uint32_t *f = &o[a].x;
                         const uint32_t *base = &pre[u][a].x;
 #pragma unroll
@@ -1071,13 +1073,14 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
 #pragma unroll
                     for (int a = 0; a < NA; ++a) o[a] = pre[u][a];
                 }
-                fetch(it + kItems, pre[u]);
+                fetch(pre[u]);
                 if ((product || in != y) && n < width)
 #pragma unroll
                     for (int a = 0; a < NA; ++a) {
                         const int t = tok[4 * a];
                         if (t >= 0) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o[a];
                     }
+                if (++nt == nt_all) nt = 0, ++lt;
             }
         tc_before();
     }
