@@ -785,13 +785,15 @@ __global__ void __launch_bounds__(kTcThreads)
 // aligned.  A persistent CTA per SM takes a run of (tile, 256 bytes of columns) items.
 // Operands: z's pieces [128 tokens][pieces x Kp] K-major, loaded once per tile; B [columns]
 // [ranks] K-major, or A [ranks][columns] MN-major, in a ring; both by TMA; D in TMEM, double
-// buffered.  Eight epilogue warps (32 tokens x 128 bytes each) turn D's rows (a TMEM lane is
-// a token) into coalesced rows through shared memory and add y_in, whose loads run 64 KB
-// ahead per SM.  Bound by reading y_in and writing y.  Measured for
+// buffered.  Sixteen epilogue warps (32 tokens x 128 bytes of every second item) turn D's
+// rows (a TMEM lane is a token) into coalesced rows through shared memory and add y_in,
+// whose loads run an item ahead, 64 KB per SM.  Bound by reading y_in and writing y.  Measured for
 // 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): EXPAND_US us;
 // a lane per token straight to memory 67 us and a lane per column 44 us (the load/store
 // unit), TMA row gathers and scatters 62 us (about 75 cycles per four rows).
-constexpr int kExpandThreads = kWorkers + 96;   // epilogue, MMA, TMA, fix warps
+constexpr int kEpiWarps = 16;
+constexpr int kExpandThreads = kEpiWarps * 32 + 96;   // epilogue, MMA, TMA, fix warps
+constexpr int kAnyThreads = kWorkers + 96;
 constexpr int kExpandNS = 4;                    // weight stages at most
 constexpr int kAnyNS = 3;
 constexpr int kMaxRun = 16;                     // tiles that a CTA's run may touch
@@ -882,13 +884,13 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], kWorkers / 32);
+            mbar_init(&tempty[i], kEpiWarps / 2);
         }
         fence_mbar_init();
     }
     pdl_wait();
     pdl_trigger();
-    if (warp == kMmaWarp) tc_alloc(&s_tmem, 256);
+    if (warp == kEpiWarps) tc_alloc(&s_tmem, 256);
     constexpr int NW = 256 / sizeof(TY), NB = 128 / sizeof(TY);   // columns of an item, of a warp
     constexpr int kUse = use_pieces<TX, TY>();
     const int Kp = p.Kp, width = kGrad ? p.K : p.N;
@@ -919,7 +921,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         ++j;
         if (++s == ns) s = 0, ph ^= 1;
     };
-    if (warp == kTmaWarp) {   // ---- copies of the operands
+    if (warp == kEpiWarps + 1) {   // ---- copies of the operands
         if (lane == 0)
             for (int it = lo; it < hi; ++it) {
                 const int lt = it / nt_all - tile0, n0 = it % nt_all * NW;
@@ -944,7 +946,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                 }
                 advance();
             }
-    } else if (warp == kTmaWarp + 1) {
+    } else if (warp == kEpiWarps + 2) {
         // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
         // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
         for (int it = lo; it < hi; ++it) {
@@ -960,7 +962,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             if (lane == 0) mbar_arrive(&wfull[s]);
             advance();
         }
-    } else if (warp == kMmaWarp) {   // ---- products
+    } else if (warp == kEpiWarps) {   // ---- products
         if (lane == 0) {
             const uint32_t idesc = idesc16<TX>(NW, false, kGrad);
             const uint64_t dz0 = sdesc_k(zs), dw0 = kGrad ? sdesc_mn(ws, Kp * 128) : sdesc_k(ws);
@@ -989,103 +991,113 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
                 advance();
             }
         }
-    } else {   // ---- epilogue: tokens [32 q4, +32), 128 bytes of columns
-        const int q4 = warp & 3, half = warp >> 2;
-        constexpr int kPitch = NB + 4;                // floats of a row of the warp's block
+    } else {
+        // ---- epilogue: tokens [32 q4, +32), 128 bytes of columns of every second item with a
+        // product (and of the others), so that sixteen warps hide one another's latencies
+        const int q4 = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
+        constexpr int kPitch = 36;                        // floats of a row of the warp's block
         float *sc = reinterpret_cast<float *>(buf + zb + ns * wb) + warp * 32 * kPitch;
-        constexpr int CE = 16 / sizeof(TY), NA = 8;   // a lane's 16 bytes, 8 lanes a row: 8 accesses of 4 rows
-        constexpr int kItems = 2;                     // items whose y_in is in flight: 8 KB a warp
-        const int rl = lane >> 3, cl = half * NB + (lane & 7) * CE;
-        uint4 pre[kItems][NA];
-        // the next item to load and the next to finish: tile of the run, block of columns
-        int f_it = lo, f_lt = 0, f_nt = lo - tile0 * nt_all, lt = f_lt, nt = f_nt;
-        auto fetch = [&](uint4 (&v)[NA]) {
-            const int n = f_nt * NW + cl;
-            const int *tok = s_tok + f_lt * kTile + q4 * 32 + rl;
-            if (in && f_it < hi && n < width)
-#pragma unroll
-                for (int a = 0; a < NA; ++a) {
-                    const int t = tok[4 * a];
-                    if (t >= 0) v[a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
-                }
-            ++f_it;
-            if (++f_nt == nt_all) f_nt = 0, ++f_lt;
+        constexpr int CE = 16 / sizeof(TY), LPR = 32 / CE, RPA = 32 / LPR;   // a lane's 16 bytes, lanes of a row, rows
+        constexpr int NP = NB / 32, NA = LPR;             // passes of 32 columns, accesses of a pass
+        const int rl = lane / LPR, cl = half * NB + lane % LPR * CE;
+        struct Item {
+            int it, lt, nt, j;
         };
+        // the next item of this group at or behind i
+        auto own = [&](Item &i) {
+            while (i.it < hi) {
+                const bool product = s_rank[i.lt] > 0;
+                if (((product ? i.j : i.it) & 1) == group) return;
+                i.j += product;
+                ++i.it;
+                if (++i.nt == nt_all) i.nt = 0, ++i.lt;
+            }
+        };
+        auto behind = [&](Item i) {
+            i.j += s_rank[i.lt] > 0;
+            ++i.it;
+            if (++i.nt == nt_all) i.nt = 0, ++i.lt;
+            own(i);
+            return i;
+        };
+        uint4 pre[NP][NA];
+        auto fetch = [&](const Item &i, int ps, int a) {
+            const int n = i.nt * NW + cl + ps * 32;
+            if (!in || i.it >= hi || n >= width) return;
+            const int t = s_tok[i.lt * kTile + q4 * 32 + a * RPA + rl];
+            if (t >= 0) pre[ps][a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
+        };
+        Item at = {lo, 0, lo - tile0 * nt_all, 0};
+        own(at);
 #pragma unroll
-        for (int u = 0; u < kItems; ++u) {
+        for (int ps = 0; ps < NP; ++ps)
 #pragma unroll
-            for (int a = 0; a < NA; ++a) pre[u][a] = make_uint4(0u, 0u, 0u, 0u);
-            fetch(pre[u]);
-        }
-        bool ok = true;
-        for (int it0 = lo; it0 < hi && ok; it0 += kItems)
+            for (int a = 0; a < NA; ++a) {
+                pre[ps][a] = make_uint4(0u, 0u, 0u, 0u);
+                fetch(at, ps, a);
+            }
+        int turn = 0;
+        while (at.it < hi) {
+            const Item next = behind(at);
+            const bool product = s_rank[at.lt] > 0;
+            float scale = 0.f;
+            if (product) {
+                const bool ok = mbar_wait(&tfull[group], turn, p.status);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                turn ^= 1;
+                tc_after();
+                scale = s_scale[at.lt * kTile + q4 * 32 + lane];
+            }
 #pragma unroll
-            for (int u = 0; u < kItems; ++u) {
-                const int it = it0 + u;
-                if (it >= hi || !ok) continue;
-                const int b = j & 1, n = nt * NW + cl;
-                const bool product = s_rank[lt] > 0;
-                const int *tok = s_tok + lt * kTile + q4 * 32 + rl;
-                uint4 o[NA];
+            for (int ps = 0; ps < NP; ++ps) {
                 if (product) {
-                    ok = mbar_wait(&tfull[b], (j >> 1) & 1, p.status);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) continue;
-                    tc_after();
-                    const float scale = s_scale[lt * kTile + q4 * 32 + lane];
 #pragma unroll
-                    for (int h = 0; h < NB; h += 32) {
-                        float v[32];
-                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + b * 128 + half * NB + h, v);
+                    for (int h = 0; h < 32; h += 16) {
+                        float v[16];
+                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + group * 128 + half * NB + ps * 32 + h, v);
                         tc_wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
+                        for (int e = 0; e < 16; e += 4)
                             *reinterpret_cast<float4 *>(sc + lane * kPitch + h + e) =
                                 make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
                     }
                     tc_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&tempty[b]);
-                    ++j;
-#pragma unroll
-                    for (int a = 0; a < NA; ++a) {
-                        float d[CE];
-                        const float *src = sc + (4 * a + rl) * kPitch + (lane & 7) * CE;
-                        if (CE == 8) {   // (lanes 4 .. 7 of a row take their halves in turn: no bank twice)
-                            const int h = lane & 4;
-                            const float4 x = *reinterpret_cast<const float4 *>(src + h);
-                            const float4 w = *reinterpret_cast<const float4 *>(src + (h ^ 4));
-                            *reinterpret_cast<float4 *>(d) = h ? w : x;
-                            *reinterpret_cast<float4 *>(d + CE - 4) = h ? x : w;
-                        } else {
-                            *reinterpret_cast<float4 *>(d) = *reinterpret_cast<const float4 *>(src);
-                        }
-                        uint32_t *f = &o[a].x;
-                        const uint32_t *base = &pre[u][a].x;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if (sizeof(TY) == 4) f[e] = add_pair<TY>(base[e], d[e % CE], 0.f);
-                            else f[e] = add_pair<TY>(base[e], d[2 * e % CE], d[(2 * e + 1) % CE]);
-                        }
-                    }
-                    __syncwarp();
-                } else {   // no product: the base's bits
-#pragma unroll
-                    for (int a = 0; a < NA; ++a) o[a] = pre[u][a];
+                    if (ps == NP - 1 && lane == 0) mbar_arrive(&tempty[group]);
                 }
-                fetch(pre[u]);
-                if ((product || in != y) && n < width)
+                const int n = at.nt * NW + cl + ps * 32;
 #pragma unroll
-                    for (int a = 0; a < NA; ++a) {
-                        const int t = tok[4 * a];
-                        if (t >= 0) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o[a];
+                for (int a = 0; a < NA; ++a) {
+                    uint4 o = pre[ps][a];
+                    if (product) {
+                        const float *d = sc + (a * RPA + rl) * kPitch + lane % LPR * CE;
+                        uint32_t *f = &o.x;
+#pragma unroll
+                        for (int h = 0; h < CE / 4; ++h) {
+                            const float4 x = *reinterpret_cast<const float4 *>(d + 4 * h);
+                            if (sizeof(TY) == 4) {
+                                f[0] = add_pair<TY>(f[0], x.x, 0.f);
+                                f[1] = add_pair<TY>(f[1], x.y, 0.f);
+                                f[2] = add_pair<TY>(f[2], x.z, 0.f);
+                                f[3] = add_pair<TY>(f[3], x.w, 0.f);
+                            } else {
+                                f[2 * h] = add_pair<TY>(f[2 * h], x.x, x.y);
+                                f[2 * h + 1] = add_pair<TY>(f[2 * h + 1], x.z, x.w);
+                            }
+                        }
                     }
-                if (++nt == nt_all) nt = 0, ++lt;
+                    const int t = s_tok[at.lt * kTile + q4 * 32 + a * RPA + rl];
+                    if (t >= 0 && n < width && (product || in != y)) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o;
+                    fetch(next, ps, a);
+                }
+                __syncwarp();
             }
+            at = next;
+        }
         tc_before();
     }
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == kEpiWarps) {
         tc_after();
         tc_dealloc(tmem, 256);
     }
@@ -1101,17 +1113,17 @@ __device__ void copy_rows(const int *tok, const TY *in, long long ld_in, TY *y, 
 {
     constexpr int CE = sizeof(C) / sizeof(TY), kU = 8;
     const int per = cols / CE, n = kTile * per;
-    for (int e0 = threadIdx.x; e0 < n; e0 += kU * kExpandThreads) {
+    for (int e0 = threadIdx.x; e0 < n; e0 += kU * kAnyThreads) {
         C v[kU];
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int e = e0 + u * kExpandThreads, t = e < n ? tok[e / per] : -1;
+            const int e = e0 + u * kAnyThreads, t = e < n ? tok[e / per] : -1;
             v[u] = C{};
             if (in && t >= 0) v[u] = *reinterpret_cast<const C *>(in + t * ld_in + e % per * CE);
         }
 #pragma unroll
         for (int u = 0; u < kU; ++u) {
-            const int e = e0 + u * kExpandThreads, t = e < n ? tok[e / per] : -1;
+            const int e = e0 + u * kAnyThreads, t = e < n ? tok[e / per] : -1;
             if (t >= 0) *reinterpret_cast<C *>(y + t * ldy + e % per * CE) = v[u];
         }
     }
@@ -1120,7 +1132,7 @@ __device__ void copy_rows(const int *tok, const TY *in, long long ld_in, TY *y, 
 // kPair: rows of 16-bit elements start at 4-byte boundaries, and two lanes share a 4-byte
 // access of neighbouring columns (one takes the even token, the other the odd one)
 template <typename TX, typename TY, bool kGrad, bool kPair>
-__global__ void __launch_bounds__(kExpandThreads, 2)
+__global__ void __launch_bounds__(kAnyThreads, 2)
     expand_any_kernel(const __grid_constant__ CUtensorMap map, const AdParams p)
 {
     extern __shared__ unsigned char raw[];
@@ -1555,7 +1567,7 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
     CUtensorMap z;
     if (width * es % 16 == 0 && rows16(p.y, p.ldy) && rows16(p.y_in, p.ldy_in) && tiles / h->num_sms + 2 <= kMaxRun) {
         if (!make_pieces_map(h, &z, p.pieces, p.T)) return cudaErrorInvalidValue;
-        const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kWorkers * (128 / es + 4) * 4;
+        const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kEpiWarps * 32 * 36 * 4;
         const size_t fixed = 1024 + expand_z_bytes(use_pieces<TX, TY>() * p.Kp) + scratch;
         const int ns = (int)std::min<size_t>(kExpandNS, (kMaxSmem - 16 * 1024 - fixed) / wb);   // (16 KB: the run's tiles)
         return launch_cluster(expand_tile_kernel<TX, TY, kGrad>, dim3(h->num_sms), kExpandThreads, fixed + ns * wb, 1, s,
@@ -1567,7 +1579,7 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
     const bool pair = width % 2 == 0 && pairs(p.y, p.ldy) && (!p.y_in || pairs(p.y_in, p.ldy_in));
     const bool two = sizeof(TY) == 2 && pair;   // (fp32 has no pairs)
     return launch_cluster(two ? expand_any_kernel<TX, TY, kGrad, sizeof(TY) == 2> : expand_any_kernel<TX, TY, kGrad, false>,
-                          dim3(tiles, groups), kExpandThreads, smem, 1, s, kGrad ? h->map_a : h->map_b, p);
+                          dim3(tiles, groups), kAnyThreads, smem, 1, s, kGrad ? h->map_a : h->map_b, p);
 }
 
 template <typename TX, bool kGrad>

@@ -75,7 +75,7 @@ __device__ __forceinline__ void tc_dealloc(uint32_t tmem, uint32_t cols)   // by
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(cols));
 }
 
-// 8 and 32 consecutive columns of this thread's TMEM lane
+// 8 and 16 consecutive columns of this thread's TMEM lane
 __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8])
 {
     uint32_t *u = reinterpret_cast<uint32_t *>(v);
@@ -84,16 +84,12 @@ __device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[8])
                  : "r"(taddr));
 }
 
-__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[32])
+__device__ __forceinline__ void tc_ld(uint32_t taddr, float (&v)[16])
 {
     uint32_t *u = reinterpret_cast<uint32_t *>(v);
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
-                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
-                   "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]),
-                   "=r"(u[23]), "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]),
-                   "=r"(u[30]), "=r"(u[31])
+                   "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
                  : "r"(taddr));
 }
 
