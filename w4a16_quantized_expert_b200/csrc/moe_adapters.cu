@@ -1494,29 +1494,6 @@ cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStr
     return launch_sort(q, s);
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
-                           const Args &...args)
-{
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 // CTAs of a cluster that share `blocks` steps of work so that `units` clusters give every SM
 // about two CTAs
 int split_of(long long units, int blocks, int num_sms)
@@ -1539,7 +1516,7 @@ cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, h->num_sms);
     const size_t ring = (size_t)kShrinkNS * (kBlk + shrink_w_bytes(kGrad, p.R, p.Kp));
     const size_t sums = (size_t)kTile * (p.Kp + 4) * 4;
-    return launch_cluster(shrink_tile_kernel<TX, kGrad>, dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s,
+    return launch_chained(shrink_tile_kernel<TX, kGrad>, {dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s},
                           kGrad ? h->map_b64 : h->map_a, p);
 }
 
@@ -1554,8 +1531,8 @@ cudaError_t run_grad(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     const size_t stage = 2 * 8192 + grad_z_bytes(kPieces<TX> * p.Kp);
     const size_t sums = (size_t)std::max(128 * (p.Kp + 4), p.Kp * 132) * 4;
     const bool four = 4 * stage <= kMaxSmem;
-    return launch_cluster(four ? grad_tile_kernel<TX, 4> : grad_tile_kernel<TX, 3>, dim3(tiles * S, p.n), kTcThreads,
-                          1024 + std::max((four ? 4 : 3) * stage, sums), S, s, dz, z, p);
+    const ChainLaunch l = {dim3(tiles * S, p.n), kTcThreads, 1024 + std::max((four ? 4 : 3) * stage, sums), S, s};
+    return launch_chained(four ? grad_tile_kernel<TX, 4> : grad_tile_kernel<TX, 3>, l, dz, z, p);
 }
 
 template <typename TX, typename TY, bool kGrad>
@@ -1570,7 +1547,7 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
         const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kEpiWarps * 32 * 36 * 4;
         const size_t fixed = 1024 + expand_z_bytes(use_pieces<TX, TY>() * p.Kp) + scratch;
         const int ns = (int)std::min<size_t>(kExpandNS, (kMaxSmem - 16 * 1024 - fixed) / wb);   // (16 KB: the run's tiles)
-        return launch_cluster(expand_tile_kernel<TX, TY, kGrad>, dim3(h->num_sms), kExpandThreads, fixed + ns * wb, 1, s,
+        return launch_chained(expand_tile_kernel<TX, TY, kGrad>, {dim3(h->num_sms), kExpandThreads, fixed + ns * wb, 1, s},
                               kGrad ? h->map_a : es == 4 ? h->map_b64 : h->map_b, z, p, ns);
     }
     const int groups = std::max(1, std::min((width + 127) / 128, 2 * h->num_sms / tiles));
@@ -1578,8 +1555,10 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
     auto pairs = [&](const void *q, long long ld) { return reinterpret_cast<uintptr_t>(q) % 4 == 0 && ld % 2 == 0; };
     const bool pair = width % 2 == 0 && pairs(p.y, p.ldy) && (!p.y_in || pairs(p.y_in, p.ldy_in));
     const bool two = sizeof(TY) == 2 && pair;   // (fp32 has no pairs)
-    return launch_cluster(two ? expand_any_kernel<TX, TY, kGrad, sizeof(TY) == 2> : expand_any_kernel<TX, TY, kGrad, false>,
-                          dim3(tiles, groups), kAnyThreads, smem, 1, s, kGrad ? h->map_a : h->map_b, p);
+    const ChainLaunch l = {dim3(tiles, groups), kAnyThreads, smem, 1, s};
+    const CUtensorMap &w = kGrad ? h->map_a : h->map_b;
+    return two ? launch_chained(expand_any_kernel<TX, TY, kGrad, sizeof(TY) == 2>, l, w, p)
+               : launch_chained(expand_any_kernel<TX, TY, kGrad, false>, l, w, p);
 }
 
 template <typename TX, bool kGrad>
@@ -1595,30 +1574,56 @@ cudaError_t run_expand(const moe_adapters *h, const AdParams &p, int y_dtype, cu
 template <typename TX, typename TY>
 cudaError_t run_few_expand(const AdParams &p, cudaStream_t s)
 {
-    const dim3 grid((p.N + kFewN - 1) / kFewN, p.T);
+    const ChainLaunch l = {dim3((p.N + kFewN - 1) / kFewN, p.T), kFewThreads, 0, 1, s};
     const int kb = p.Kp / 16;
-    if (kb <= 1) return launch_chained(expand_few_kernel<TX, TY, 1>, grid, kFewThreads, 0, s, p);
-    if (kb <= 2) return launch_chained(expand_few_kernel<TX, TY, 2>, grid, kFewThreads, 0, s, p);
-    if (kb <= 4) return launch_chained(expand_few_kernel<TX, TY, 4>, grid, kFewThreads, 0, s, p);
-    return launch_chained(expand_few_kernel<TX, TY, 8>, grid, kFewThreads, 0, s, p);
+    if (kb <= 1) return launch_chained(expand_few_kernel<TX, TY, 1>, l, p);
+    if (kb <= 2) return launch_chained(expand_few_kernel<TX, TY, 2>, l, p);
+    if (kb <= 4) return launch_chained(expand_few_kernel<TX, TY, 4>, l, p);
+    return launch_chained(expand_few_kernel<TX, TY, 8>, l, p);
 }
 
 template <typename TX>
 cudaError_t run_few(const AdParams &p, int y_dtype, cudaStream_t s)
 {
-    const dim3 grid(p.splits, p.T);
+    const ChainLaunch l = {dim3(p.splits, p.T), kFewThreads, 0, 1, s};
     const int nb = p.R / 8;
-    const cudaError_t e = nb <= 1   ? launch_chained(shrink_few_kernel<TX, 1>, grid, kFewThreads, 0, s, p)
-                          : nb <= 2 ? launch_chained(shrink_few_kernel<TX, 2>, grid, kFewThreads, 0, s, p)
-                          : nb <= 4 ? launch_chained(shrink_few_kernel<TX, 4>, grid, kFewThreads, 0, s, p)
-                          : nb <= 8 ? launch_chained(shrink_few_kernel<TX, 8>, grid, kFewThreads, 0, s, p)
-                                    : launch_chained(shrink_few_kernel<TX, 16>, grid, kFewThreads, 0, s, p);
+    const cudaError_t e = nb <= 1   ? launch_chained(shrink_few_kernel<TX, 1>, l, p)
+                          : nb <= 2 ? launch_chained(shrink_few_kernel<TX, 2>, l, p)
+                          : nb <= 4 ? launch_chained(shrink_few_kernel<TX, 4>, l, p)
+                          : nb <= 8 ? launch_chained(shrink_few_kernel<TX, 8>, l, p)
+                                    : launch_chained(shrink_few_kernel<TX, 16>, l, p);
     if (e != cudaSuccess) return e;
     switch (y_dtype) {
     case MOE_DTYPE_F16: return run_few_expand<TX, __half>(p, s);
     case MOE_DTYPE_BF16: return run_few_expand<TX, __nv_bfloat16>(p, s);
     default: return run_few_expand<TX, float>(p, s);
     }
+}
+
+template <typename TX, typename TY>
+cudaError_t prepare_expand()
+{
+    cudaError_t e = allow_smem(expand_tile_kernel<TX, TY, false>);
+    if (e == cudaSuccess) e = allow_smem(expand_tile_kernel<TX, TY, true>);
+    if (e == cudaSuccess) e = allow_smem(expand_any_kernel<TX, TY, false, false>);
+    if (e == cudaSuccess) e = allow_smem(expand_any_kernel<TX, TY, true, false>);
+    if (e == cudaSuccess && sizeof(TY) == 2) e = allow_smem(expand_any_kernel<TX, TY, false, sizeof(TY) == 2>);
+    if (e == cudaSuccess && sizeof(TY) == 2) e = allow_smem(expand_any_kernel<TX, TY, true, sizeof(TY) == 2>);
+    return e;
+}
+
+// shared-memory limits of the kernels that a pool's calls launch
+template <typename TX>
+cudaError_t prepare()
+{
+    cudaError_t e = sort_prepare();
+    if (e == cudaSuccess) e = allow_smem(shrink_tile_kernel<TX, false>);
+    if (e == cudaSuccess) e = allow_smem(shrink_tile_kernel<TX, true>);
+    if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 3>);
+    if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 4>);
+    if (e == cudaSuccess) e = prepare_expand<TX, __half>();
+    if (e == cudaSuccess) e = prepare_expand<TX, __nv_bfloat16>();
+    return e == cudaSuccess ? prepare_expand<TX, float>() : e;
 }
 
 template <typename TX>
@@ -1636,7 +1641,7 @@ cudaError_t run_backward(const moe_adapters *h, const AdParams &p, int dx_dtype,
     cudaError_t e = run_sort(h, p, ws, s);
     if (e == cudaSuccess && p.T) e = run_shrink<TX, true>(h, p, s);
     if (e == cudaSuccess && p.want_dw && p.T && !TcType<TX>::code)
-        e = launch_chained(pieces_kernel, dim3(tiles_max(h->desc, p.T) * (kTile / (kWorkers / 32))), kWorkers, 0, s, p);
+        e = launch_chained(pieces_kernel, {dim3(tiles_max(h->desc, p.T) * (kTile / (kWorkers / 32))), kWorkers, 0, 1, s}, p);
     if (e == cudaSuccess && p.want_dw) e = run_grad<TX>(h, p, s);
     return e != cudaSuccess || !p.y ? e : run_expand<TX, true>(h, p, dx_dtype, s);
 }
@@ -1673,6 +1678,7 @@ int moe_adapters_create(const moe_adapters_desc *desc, const moe_adapters_weight
         !make_pool_map(&h->map_a, w.a, d.in_features, d.max_rank, d.n_adapters, rank_pad(d)) ||
         !make_pool_map(&h->map_b, w.b, d.max_rank, d.out_features, d.n_adapters, 128) ||
         !make_pool_map(&h->map_b64, w.b, d.max_rank, d.out_features, d.n_adapters, 64) ||
+        (d.dtype == MOE_DTYPE_F16 ? prepare<__half>() : prepare<__nv_bfloat16>()) != cudaSuccess ||
         cudaMalloc(&h->d_status, 256) != cudaSuccess) {
         delete h;
         return MOE_ERR_CUDA;

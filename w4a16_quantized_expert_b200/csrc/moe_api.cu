@@ -573,7 +573,8 @@ int moe_layer_create(const moe_layer_desc *desc, const moe_weights *weights, moe
         delete L;
         return MOE_ERR_CUDA;
     }
-    bool occ_ok = router_prepare() == cudaSuccess && ffn_prepare(d.format, d.n_experts, L->occ) == cudaSuccess &&
+    bool occ_ok = router_prepare() == cudaSuccess && sort_prepare() == cudaSuccess &&
+                  ffn_prepare(d.format, d.n_experts, L->occ) == cudaSuccess &&
                   (d.format != MOE_FMT_INT4_ROWSCALE || tc_prepare(d.n_experts) == cudaSuccess) &&
                   (!fused_format(d.format) ||
                    (fused_prepare(d.format, &L->occ_fused) == cudaSuccess && L->occ_fused >= 1));

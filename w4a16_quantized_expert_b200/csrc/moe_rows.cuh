@@ -86,21 +86,46 @@ __device__ __forceinline__ Vec8<T> pack8(const float (&f)[8])
 
 // launches with the programmatic-serialisation attribute: the kernel may start while its
 // predecessor on the stream drains, and waits for it (pdl_wait) before touching memory
+struct ChainLaunch {
+    dim3 grid;
+    int threads;
+    size_t smem;
+    int cluster;   // CTAs (x) of a cluster
+    cudaStream_t stream;
+};
+
 template <typename... KArgs, typename... Args>
-cudaError_t launch_chained(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s,
-                           Args &&...args)
+cudaError_t launch_chained(void (*kernel)(KArgs...), const ChainLaunch &l, const Args &...args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cfg.gridDim = l.grid;
+    cfg.blockDim = dim3(l.threads);
+    cfg.dynamicSmemBytes = l.smem;
+    cfg.stream = l.stream;
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = l.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+    cfg.numAttrs = l.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// lets a kernel take all the dynamic shared memory that the device's opt-in limit leaves
+// beside its static shared memory (once per device, when a handle is created)
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...))
+{
+    cudaFuncAttributes a;
+    int dev = 0, limit = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&limit, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, kernel);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit - (int)a.sharedSizeBytes);
 }
 
 // A stable sort of n small keys (moe_sort.cu): positions of the keys' entries when the
@@ -123,5 +148,6 @@ struct SortParams {
 
 constexpr int kSortChunk = 2048;   // entries per CTA of the sort
 cudaError_t launch_sort(const SortParams &p, cudaStream_t s);
+cudaError_t sort_prepare();   // once per device
 
 }  // namespace moe

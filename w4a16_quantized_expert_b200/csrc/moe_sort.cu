@@ -2,6 +2,7 @@
 // (dispatch), their weighted way back, and the gradients of both.
 #include "moe_internal.h"
 #include "moe_rows.cuh"
+#include "moe_tcgen05.cuh"
 
 #include <algorithm>
 
@@ -11,6 +12,7 @@ namespace {
 
 constexpr int kSortThreads = 256;
 constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortCluster = 8;   // chunks of a cluster
 constexpr int kRowThreads = 256;
 
 // the bin of a key, or -1 for an entry that is dropped; other keys than -1 that lie
@@ -52,7 +54,7 @@ __device__ void block_scan(int *v, int E, int *warp_sums)
     __syncthreads();
 }
 
-// Histogram of each chunk of kSortChunk keys.
+// Histogram of each chunk of kSortChunk keys (more chunks than a cluster holds).
 __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortParams p)
 {
     extern __shared__ int s_hist[];
@@ -71,8 +73,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortParams p)
 
 // Positions of one chunk's entries: a warp owns 256 consecutive entries and ranks them 32
 // at a time (match_any: entries of equal key in lane order), which keeps the sort stable;
-// the chunks before give each bin's base.  Work is O(n + chunks * E); for the layer's
-// batches it is latency: one pass over the keys, a scan of E counts, one write.
+// the chunks before give each bin's base.  Up to 8 chunks (16384 entries) are one cluster,
+// whose CTAs read one another's counts from shared memory; more take them from
+// sort_hist_kernel.  Work is O(n + chunks * E); for the layer's batches it is latency: one
+// pass over the keys, a scan of E counts, one write.
+template <bool kCluster>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
 {
     extern __shared__ int sm[];
@@ -80,6 +85,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
     int *seg = wh + kSortWarps * p.E;      // [E + 1]
     int *base = seg + p.E + 1;             // [E] entries of the bin in the chunks before
     int *all = base + p.E;                 // [E] entries of the bin
+    int *own = all + p.E;                  // [E] entries of the bin in this chunk
     __shared__ int warp_sums[kSortWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = blockIdx.x, chunks = gridDim.x;
@@ -115,15 +121,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
             wh[w * p.E + e] = run;
             run += c;
         }
-        int before = 0, total = run;
-        if (chunks > 1) {
-            total = 0;
+        own[e] = run;
+    }
+    if (kCluster) cluster_sync();   // (a thread reads its own bins: no barrier without peers)
+    for (int e = tid; e < p.E; e += kSortThreads) {
+        int before = 0, total = 0;
+        if (kCluster) {
+            int part[kSortCluster];
+#pragma unroll
+            for (int c = 0; c < kSortCluster; ++c)
+                part[c] = c < chunks ? __float_as_int(ld_cluster(peer_addr(smem_u32(own + e), c))) : 0;
+#pragma unroll
+            for (int c = 0; c < kSortCluster; ++c) {
+                before += c < chunk ? part[c] : 0;
+                total += part[c];
+            }
+        } else if (chunks > 1) {
 #pragma unroll 4
             for (int c = 0; c < chunks; ++c) {
                 const int h = __ldcg(p.hist + (size_t)c * p.E + e);
                 before += c < chunk ? h : 0;
                 total += h;
             }
+        } else {
+            total = own[e];
         }
         base[e] = before;
         all[e] = total;
@@ -155,6 +176,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
     if (p.entry_of && chunk == 0)
         for (int e = warp; e < p.E; e += kSortWarps)
             for (int pos = seg[e] + all[e] + lane; pos < seg[e + 1]; pos += 32) p.entry_of[pos] = -1;
+    if (kCluster) cluster_sync();   // no CTA leaves while a peer reads its counts
 }
 
 // ---------------------------------------------------------------------------- rows out
@@ -389,15 +411,23 @@ cudaError_t by_type(int dtype, F &&f)
 
 }  // namespace
 
+cudaError_t sort_prepare()
+{
+    const cudaError_t e = allow_smem(sort_place_kernel<false>);
+    return e != cudaSuccess ? e : allow_smem(sort_place_kernel<true>);
+}
+
 cudaError_t launch_sort(const SortParams &p, cudaStream_t s)
 {
     const int chunks = std::max(1, (p.n + kSortChunk - 1) / kSortChunk);
+    const size_t smem = ((size_t)(kSortWarps + 4) * p.E + 1) * 4;   // at most 49,204 bytes (1025 bins)
+    if (chunks > 1 && chunks <= kSortCluster)
+        return launch_chained(sort_place_kernel<true>, {dim3(chunks), kSortThreads, smem, chunks, s}, p);
     if (chunks > 1) {
-        const cudaError_t e = launch_chained(sort_hist_kernel, dim3(chunks), kSortThreads, (size_t)p.E * 4, s, p);
+        const cudaError_t e = launch_chained(sort_hist_kernel, {dim3(chunks), kSortThreads, (size_t)p.E * 4, 1, s}, p);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = ((size_t)(kSortWarps + 3) * p.E + 1) * 4;   // at most 45,104 bytes (1025 bins)
-    return launch_chained(sort_place_kernel, dim3(chunks), kSortThreads, smem, s, p);
+    return launch_chained(sort_place_kernel<false>, {dim3(chunks), kSortThreads, smem, 1, s}, p);
 }
 
 cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k, int E, int align,
@@ -416,7 +446,7 @@ cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, 
     p.counts = counts;
     p.seg = seg;
     const int slices = row_slices(T, (p.row16 + kRowThreads - 1) / kRowThreads, num_sms);
-    return launch_chained(sort_copy_kernel, dim3(T + (align > 1 ? E : 0), slices), kRowThreads, 0, s, p);
+    return launch_chained(sort_copy_kernel, {dim3(T + (align > 1 ? E : 0), slices), kRowThreads, 0, 1, s}, p);
 }
 
 cudaError_t launch_unsort(const void *rows, int rows_dtype, int n_rows, const int32_t *row_of, const float *w, int T,
@@ -427,7 +457,7 @@ cudaError_t launch_unsort(const void *rows, int rows_dtype, int n_rows, const in
     const int slices = row_slices(T, (H / 8 + kRowThreads - 1) / kRowThreads, num_sms);
     return by_type(rows_dtype, [&](auto tr) {
         return by_type(y_dtype, [&](auto ty) {
-            return launch_chained(unsort_kernel<decltype(tr), decltype(ty)>, dim3(T, slices), kRowThreads, 0, s, p);
+            return launch_chained(unsort_kernel<decltype(tr), decltype(ty)>, {dim3(T, slices), kRowThreads, 0, 1, s}, p);
         });
     });
 }
@@ -456,13 +486,13 @@ cudaError_t launch_unsort_grad(const void *dy, int dy_dtype, long long lddy, con
     const int n = T * k;
     const bool few = n < 8 * 2 * num_sms;   // a CTA per assignment while warps would leave SMs idle
     p.n_blocks = few ? n : (n + kRowThreads / 32 - 1) / (kRowThreads / 32);
-    const dim3 grid(p.n_blocks + (seg ? E : 0));
+    const ChainLaunch l = {dim3(p.n_blocks + (seg ? E : 0)), kRowThreads, 0, 1, s};
     return by_type(rows_dtype, [&](auto tr) {
         return by_type(dy_dtype, [&](auto td) {
             using R = decltype(tr);
             using D = decltype(td);
-            return few ? launch_chained(unsort_grad_kernel<R, D, kRowThreads / 32>, grid, kRowThreads, 0, s, p)
-                       : launch_chained(unsort_grad_kernel<R, D, 1>, grid, kRowThreads, 0, s, p);
+            return few ? launch_chained(unsort_grad_kernel<R, D, kRowThreads / 32>, l, p)
+                       : launch_chained(unsort_grad_kernel<R, D, 1>, l, p);
         });
     });
 }
