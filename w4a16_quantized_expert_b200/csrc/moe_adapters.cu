@@ -1616,8 +1616,7 @@ cudaError_t prepare_expand()
 template <typename TX>
 cudaError_t prepare()
 {
-    cudaError_t e = sort_prepare();
-    if (e == cudaSuccess) e = allow_smem(shrink_tile_kernel<TX, false>);
+    cudaError_t e = allow_smem(shrink_tile_kernel<TX, false>);
     if (e == cudaSuccess) e = allow_smem(shrink_tile_kernel<TX, true>);
     if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 3>);
     if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 4>);

@@ -13,9 +13,8 @@
 #include "moe_rows.cuh"
 
 namespace moe {
-cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k, int E, int align,
-                             void *rows, const int32_t *row_of, const int32_t *counts, const int32_t *seg,
-                             int num_sms, cudaStream_t s);
+cudaError_t launch_sort_rows(const SortParams &s, const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k,
+                             void *rows, int num_sms, cudaStream_t stream);
 cudaError_t launch_unsort(const void *rows, int rows_dtype, int n_rows, const int32_t *row_of, const float *w, int T,
                           int k, int H, const float *shared, void *y, int y_dtype, long long ldy, int *status,
                           int num_sms, cudaStream_t s);
@@ -573,8 +572,7 @@ int moe_layer_create(const moe_layer_desc *desc, const moe_weights *weights, moe
         delete L;
         return MOE_ERR_CUDA;
     }
-    bool occ_ok = router_prepare() == cudaSuccess && sort_prepare() == cudaSuccess &&
-                  ffn_prepare(d.format, d.n_experts, L->occ) == cudaSuccess &&
+    bool occ_ok = router_prepare() == cudaSuccess && ffn_prepare(d.format, d.n_experts, L->occ) == cudaSuccess &&
                   (d.format != MOE_FMT_INT4_ROWSCALE || tc_prepare(d.n_experts) == cudaSuccess) &&
                   (!fused_format(d.format) ||
                    (fused_prepare(d.format, &L->occ_fused) == cudaSuccess && L->occ_fused >= 1));
@@ -770,11 +768,8 @@ int moe_sort_tokens(const moe_layer *L, const void *x, int dtype, int64_t ldx, c
     p.row_of = row_of;
     p.hist = at<int32_t>(ws, ws_layout(d, 0).ctr_end);
     p.status = L->d_status;
-    const cudaError_t e = launch_sort(p, s);
-    if (e != cudaSuccess || T == 0) return cuda_status(e);
     const size_t es = dtype_bytes(dtype);
-    return cuda_status(launch_sort_copy(x, (size_t)ldx * es, (size_t)d.hidden * es, T, d.top_k, d.n_experts, align,
-                                        rows, row_of, counts, seg_offsets, L->num_sms, s));
+    return cuda_status(launch_sort_rows(p, x, (size_t)ldx * es, (size_t)d.hidden * es, T, d.top_k, rows, L->num_sms, s));
 }
 
 int moe_sort_tokens_backward(const moe_layer *L, const void *drows, int rows_dtype, size_t n_rows,

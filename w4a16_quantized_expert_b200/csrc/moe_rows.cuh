@@ -148,6 +148,5 @@ struct SortParams {
 
 constexpr int kSortChunk = 2048;   // entries per CTA of the sort
 cudaError_t launch_sort(const SortParams &p, cudaStream_t s);
-cudaError_t sort_prepare();   // once per device
 
 }  // namespace moe

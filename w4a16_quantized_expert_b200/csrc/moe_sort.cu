@@ -81,11 +81,11 @@ template <bool kCluster>
 __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
 {
     extern __shared__ int sm[];
-    int *wh = sm;                          // [kSortWarps][E]: entries of each bin per warp
-    int *seg = wh + kSortWarps * p.E;      // [E + 1]
+    int *seg = sm;                         // [E + 1]
     int *base = seg + p.E + 1;             // [E] entries of the bin in the chunks before
     int *all = base + p.E;                 // [E] entries of the bin
     int *own = all + p.E;                  // [E] entries of the bin in this chunk
+    uint16_t *wh = reinterpret_cast<uint16_t *>(own + p.E);   // [kSortWarps][E]: entries of each bin per warp
     __shared__ int warp_sums[kSortWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int chunk = blockIdx.x, chunks = gridDim.x;
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
         int before = 0;
         if (bin[it] >= 0) before = wh[warp * p.E + bin[it]];
         __syncwarp();
-        if (bin[it] >= 0 && (same & ((1u << lane) - 1u)) == 0u) wh[warp * p.E + bin[it]] = before + __popc(same);
+        if (bin[it] >= 0 && (same & ((1u << lane) - 1u)) == 0u) wh[warp * p.E + bin[it]] = static_cast<uint16_t>(before + __popc(same));
         __syncwarp();
         rank[it] = before + __popc(same & ((1u << lane) - 1u));
     }
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
 #pragma unroll
         for (int w = 0; w < kSortWarps; ++w) {
             const int c = wh[w * p.E + e];
-            wh[w * p.E + e] = run;
+            wh[w * p.E + e] = static_cast<uint16_t>(run);
             run += c;
         }
         own[e] = run;
@@ -192,24 +192,10 @@ struct CopyParams {
     const int32_t *row_of, *counts, *seg;
 };
 
-__global__ void __launch_bounds__(kRowThreads) sort_copy_kernel(CopyParams p)
+// one CTA's slice of token t's row to the rows s_row[0 .. k)
+__device__ __forceinline__ void copy_token(const CopyParams &p, int t, const int *s_row)
 {
-    __shared__ int s_row[kMaxTopK];
-    const int tid = threadIdx.x;
-    pdl_trigger();
-    pdl_wait();
-    const int stride = gridDim.y * kRowThreads, i0 = blockIdx.y * kRowThreads + tid;
-    if ((int)blockIdx.x >= p.T) {
-        const int e = blockIdx.x - p.T;
-        const int lo = p.seg[e] + p.counts[e], hi = p.seg[e + 1];
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        for (int r = lo; r < hi; ++r)
-            for (int i = i0; i < p.row16; i += stride) p.rows[(size_t)r * p.row16 + i] = z;
-        return;
-    }
-    const int t = blockIdx.x;
-    if (tid < p.k) s_row[tid] = p.row_of[(size_t)t * p.k + tid];
-    __syncthreads();
+    const int stride = gridDim.y * kRowThreads, i0 = blockIdx.y * kRowThreads + threadIdx.x;
     const uint4 *src = p.x + (size_t)t * p.ldx;
     constexpr int kU = 4;
     for (int b = i0; b < p.row16; b += kU * stride) {
@@ -226,6 +212,84 @@ __global__ void __launch_bounds__(kRowThreads) sort_copy_kernel(CopyParams p)
                 if (b + u * stride < p.row16) dst[u * stride] = v[u];
         }
     }
+}
+
+// one CTA's slice of the padding rows [lo, hi)
+__device__ __forceinline__ void zero_rows(const CopyParams &p, int lo, int hi)
+{
+    const int stride = gridDim.y * kRowThreads, i0 = blockIdx.y * kRowThreads + threadIdx.x;
+    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+    for (int r = lo; r < hi; ++r)
+        for (int i = i0; i < p.row16; i += stride) p.rows[(size_t)r * p.row16 + i] = z;
+}
+
+__global__ void __launch_bounds__(kRowThreads) sort_copy_kernel(CopyParams p)
+{
+    __shared__ int s_row[kMaxTopK];
+    const int tid = threadIdx.x, t = blockIdx.x;
+    pdl_trigger();
+    pdl_wait();
+    if (t >= p.T) {
+        const int e = t - p.T;
+        zero_rows(p, p.seg[e] + p.counts[e], p.seg[e + 1]);
+        return;
+    }
+    if (tid < p.k) s_row[tid] = p.row_of[(size_t)t * p.k + tid];
+    __syncthreads();
+    copy_token(p, t, s_row);
+}
+
+// The sort and the copy of a decode-sized batch (at most kSmallSort assignments) in one
+// launch: every CTA counts all the keys itself (a few per thread), scans the counts and ranks
+// its own token's assignments, so that nothing waits for another CTA.  One token of 6144
+// fp16 and 8 of 256 experts: SMALL_US us a call in a graph, two launches 4.3.
+constexpr int kSmallSort = 512;
+
+__global__ void __launch_bounds__(kRowThreads) sort_small_kernel(SortParams s, CopyParams p)
+{
+    extern __shared__ int sm[];
+    int *key = sm;                 // [n] bins
+    int *cnt = key + s.n;          // [E]
+    int *seg = cnt + s.E;          // [E + 1]
+    __shared__ int warp_sums[kSortWarps];
+    __shared__ int s_row[kMaxTopK];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, t = blockIdx.x;
+    const bool first = t == 0 && blockIdx.y == 0;
+    pdl_trigger();
+    for (int e = tid; e < s.E; e += kRowThreads) cnt[e] = 0;
+    pdl_wait();
+    __syncthreads();
+    for (int i = tid; i < s.n; i += kRowThreads) {
+        const int e = bin_of(s.key[i], s.E, -1, first ? s.status : nullptr);
+        key[i] = e;
+        if (e >= 0) atomicAdd(cnt + e, 1);
+    }
+    __syncthreads();
+    for (int e = tid; e < s.E; e += kRowThreads) seg[e] = (cnt[e] + s.align - 1) / s.align * s.align;
+    __syncthreads();
+    block_scan(seg, s.E, warp_sums);
+    if (first)
+        for (int e = tid; e <= s.E; e += kRowThreads) {
+            s.seg[e] = seg[e];
+            if (e < s.E) s.counts[e] = cnt[e];
+        }
+    if (t >= p.T) {
+        const int e = t - p.T;
+        zero_rows(p, seg[e] + cnt[e], seg[e + 1]);
+        return;
+    }
+    for (int j = warp; j < p.k; j += kSortWarps) {   // the assignments before mine that share my expert
+        const int a = t * p.k + j, e = key[a];
+        int before = 0;
+        for (int i = lane; i < a; i += 32) before += key[i] == e;
+        before = __reduce_add_sync(0xffffffffu, before);
+        if (lane == 0) {
+            s_row[j] = e < 0 ? -1 : seg[e] + before;
+            if (blockIdx.y == 0) s.row_of[a] = s_row[j];
+        }
+    }
+    __syncthreads();
+    copy_token(p, t, s_row);
 }
 
 // ---------------------------------------------------------------------------- rows back
@@ -411,16 +475,10 @@ cudaError_t by_type(int dtype, F &&f)
 
 }  // namespace
 
-cudaError_t sort_prepare()
-{
-    const cudaError_t e = allow_smem(sort_place_kernel<false>);
-    return e != cudaSuccess ? e : allow_smem(sort_place_kernel<true>);
-}
-
 cudaError_t launch_sort(const SortParams &p, cudaStream_t s)
 {
     const int chunks = std::max(1, (p.n + kSortChunk - 1) / kSortChunk);
-    const size_t smem = ((size_t)(kSortWarps + 4) * p.E + 1) * 4;   // at most 49,204 bytes (1025 bins)
+    const size_t smem = (size_t)(4 * p.E + 1) * 4 + (size_t)kSortWarps * p.E * 2;   // 32,804 bytes at most (1025 bins)
     if (chunks > 1 && chunks <= kSortCluster)
         return launch_chained(sort_place_kernel<true>, {dim3(chunks), kSortThreads, smem, chunks, s}, p);
     if (chunks > 1) {
@@ -430,9 +488,9 @@ cudaError_t launch_sort(const SortParams &p, cudaStream_t s)
     return launch_chained(sort_place_kernel<false>, {dim3(chunks), kSortThreads, smem, 1, s}, p);
 }
 
-cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k, int E, int align,
-                             void *rows, const int32_t *row_of, const int32_t *counts, const int32_t *seg,
-                             int num_sms, cudaStream_t s)
+// the sort of `s` and the copy of its rows
+cudaError_t launch_sort_rows(const SortParams &s, const void *x, size_t ldx_bytes, size_t row_bytes, int T, int k,
+                             void *rows, int num_sms, cudaStream_t stream)
 {
     CopyParams p = {};
     p.x = static_cast<const uint4 *>(x);
@@ -441,12 +499,18 @@ cudaError_t launch_sort_copy(const void *x, size_t ldx_bytes, size_t row_bytes, 
     p.row16 = (int)(row_bytes / 16);
     p.T = T;
     p.k = k;
-    p.E = E;
-    p.row_of = row_of;
-    p.counts = counts;
-    p.seg = seg;
+    p.E = s.E;
+    p.row_of = s.row_of;
+    p.counts = s.counts;
+    p.seg = s.seg;
     const int slices = row_slices(T, (p.row16 + kRowThreads - 1) / kRowThreads, num_sms);
-    return launch_chained(sort_copy_kernel, {dim3(T + (align > 1 ? E : 0), slices), kRowThreads, 0, 1, s}, p);
+    ChainLaunch l = {dim3(T + (s.align > 1 ? s.E : 0), slices), kRowThreads, 0, 1, stream};
+    if (T > 0 && s.n <= kSmallSort) {
+        l.smem = (size_t)(s.n + 2 * s.E + 1) * 4;
+        return launch_chained(sort_small_kernel, l, s, p);
+    }
+    const cudaError_t e = launch_sort(s, stream);
+    return e != cudaSuccess || T == 0 ? e : launch_chained(sort_copy_kernel, l, p);
 }
 
 cudaError_t launch_unsort(const void *rows, int rows_dtype, int n_rows, const int32_t *row_of, const float *w, int T,

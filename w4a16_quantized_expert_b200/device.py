@@ -24,11 +24,26 @@ _DTYPE = {torch.float16: MOE_DTYPE_F16, torch.uint16: MOE_DTYPE_F16, torch.bfloa
 
 def _rows(t: torch.Tensor, shape: tuple, what: str) -> tuple:
     """(address, MOE_DTYPE_*, row stride) of a 2-D tensor whose rows are dense."""
-    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1) or t.dtype not in _DTYPE or not t.is_cuda:
+    dtype = _DTYPE.get(t.dtype)
+    if t.shape != shape or dtype is None or not t.is_cuda:
+        stride = None
+    else:
+        stride = t.stride()
+    if stride is None or (stride[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what}: a CUDA tensor {list(shape)} of fp16, bf16 or fp32 with dense rows is wanted, "
-                         f"got {t.dtype} {list(t.shape)} with strides {t.stride()}")
+                         f"got {t.dtype} {list(t.shape)} with strides {t.stride()} on {t.device}")
     # (the stride of a single row may be any number)
-    return t.data_ptr(), _DTYPE[t.dtype], t.stride(0) if shape[0] > 1 else shape[1]
+    return t.data_ptr(), dtype, stride[0] if shape[0] > 1 else shape[1]
+
+
+def _raw_stream(stream, index: int) -> int:
+    """Handle of a stream, or of the current stream of device `index` (looked up without
+    making a torch.cuda.Stream, which takes longer than a small launch)."""
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(index)
+
+
+def _index(device: torch.device) -> int:
+    return torch.cuda.current_device() if device.index is None else device.index
 
 
 def _dense(t: torch.Tensor, dtype, numel: int, what: str) -> int:
@@ -80,6 +95,7 @@ class DeviceLayer:
         self.weights = w
         self.desc = make_desc(self.d, max_tokens)
         self.handle = moe_layer_create(self.desc, self.weights)
+        self.index = _index(self.device)
 
     def clone_weights(self) -> "DeviceLayer":
         """A second layer with the same values at different HBM addresses."""
@@ -202,7 +218,7 @@ class DeviceLayer:
                         _dense(rows, x.dtype, rows.shape[0] * H, "rows"), rows.shape[0],
                         _dense(row_of, torch.int32, T * k, "row_of"), _dense(counts, torch.int32, E, "counts"),
                         _dense(seg, torch.int32, E + 1, "seg_offsets"), ws.data_ptr(), ws.numel(),
-                        self._stream(stream))
+                        _raw_stream(stream, self.index))
         return out
 
     def sort_tokens_backward(self, drows, row_of, dx=None, stream=None):
@@ -214,7 +230,7 @@ class DeviceLayer:
         pr, rdt = _dense(drows, drows.dtype, n * H, "drows"), _DTYPE[drows.dtype]
         px, xdt, ldx = _rows(dx, (T, H), "dx")
         moe_sort_tokens_backward(self.handle, pr, rdt, n, _dense(row_of, torch.int32, T * k, "row_of"), T, px, xdt,
-                                 ldx, self._stream(stream))
+                                 ldx, _raw_stream(stream, self.index))
         return dx
 
     def unsort_tokens(self, rows, row_of, topk_w, y_shared=None, y=None, stream=None):
@@ -228,7 +244,7 @@ class DeviceLayer:
                           _dense(row_of, torch.int32, T * k, "row_of"),
                           _dense(topk_w, torch.float32, T * k, "topk_w"),
                           None if y_shared is None else _dense(y_shared, torch.float32, T * H, "y_shared"), T, py,
-                          ydt, ldy, self._stream(stream))
+                          ydt, ldy, _raw_stream(stream, self.index))
         return y
 
     def unsort_tokens_backward(self, dy, rows, row_of, topk_w, counts=None, seg_offsets=None, out=None, stream=None):
@@ -247,7 +263,7 @@ class DeviceLayer:
                                    None if seg_offsets is None else
                                    _dense(seg_offsets, torch.int32, E + 1, "seg_offsets"), T,
                                    _dense(drows, rows.dtype, n * H, "drows"),
-                                   _dense(dw, torch.float32, T * k, "dw"), self._stream(stream))
+                                   _dense(dw, torch.float32, T * k, "dw"), _raw_stream(stream, self.index))
         return out
 
 
@@ -269,6 +285,7 @@ class DeviceAdapters:
         self.desc = moe_adapters_desc(in_features=K, out_features=N, n_adapters=n, max_rank=R,
                                       dtype=_DTYPE[a.dtype], max_tokens=max_tokens)
         self.handle = moe_adapters_create(self.desc, w)
+        self.index = _index(self.device)
 
     def close(self):
         if getattr(self, "handle", None):
@@ -316,7 +333,7 @@ class DeviceAdapters:
         pb, ldb = self._base(y_in, y, (T, self.N), "y_in")
         moe_adapters_apply(self.handle, px, ldx, _dense(adapter_of, torch.int32, T, "adapter_of"), T, pb, ldb, py, ydt,
                            ldy, None if z is None else _dense(z, torch.float32, T * self.R, "z"), ws.data_ptr(),
-                           ws.numel(), DeviceLayer._stream(stream))
+                           ws.numel(), _raw_stream(stream, self.index))
         return y
 
     def backward(self, x, z, dy, adapter_of, ws, dx_in=None, dx=None, da=None, db=None, accumulate=False,
@@ -343,7 +360,7 @@ class DeviceAdapters:
             pz = _dense(z, torch.float32, T * self.R, "z")
         moe_adapters_backward(self.handle, px, ldx, pz, pdy, lddy, _dense(adapter_of, torch.int32, T, "adapter_of"), T,
                               pin, ldi, pdx, ddt, lddx, pa, pb, int(accumulate), ws.data_ptr(), ws.numel(),
-                              DeviceLayer._stream(stream))
+                              _raw_stream(stream, self.index))
         return (dx if want_dx else None), (da if want_dw else None), (db if want_dw else None)
 
 
