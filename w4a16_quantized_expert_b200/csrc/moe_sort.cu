@@ -63,8 +63,9 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(SortParams p)
     pdl_wait();
     __syncthreads();
     const int base = blockIdx.x * kSortChunk, end = min(base + kSortChunk, p.n);
+#pragma unroll 8
     for (int i = base + threadIdx.x; i < end; i += kSortThreads) {
-        const int e = bin_of(p.key[i], key_bins(p), p.none_bin, nullptr);
+        const int e = bin_of(__ldcg(p.key + i), key_bins(p), p.none_bin, nullptr);
         if (e >= 0) atomicAdd(s_hist + e, 1);   // (integer counts: any order gives the same)
     }
     __syncthreads();
@@ -98,10 +99,13 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
     const int first = chunk * kSortChunk + warp * (kIter * 32) + lane;
     int bin[kIter], rank[kIter];
 #pragma unroll
-    for (int it = 0; it < kIter; ++it) {
+    for (int it = 0; it < kIter; ++it) {   // (all the loads first: recording a bad key would order them)
         const int i = first + it * 32;
-        bin[it] = i < p.n ? bin_of(p.key[i], key_bins(p), p.none_bin, p.status) : -1;
+        bin[it] = i < p.n ? __ldcg(p.key + i) : -1;
     }
+#pragma unroll
+    for (int it = 0; it < kIter; ++it)
+        bin[it] = first + it * 32 < p.n ? bin_of(bin[it], key_bins(p), p.none_bin, p.status) : -1;
 #pragma unroll
     for (int it = 0; it < kIter; ++it) {
         const unsigned same = __match_any_sync(0xffffffffu, bin[it]);
