@@ -368,45 +368,77 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
 // anywhere; row gathers by TMA were slower: 26 against 21 us for the shrink of 4096 tokens of
 // 6144) and leaves an arrival behind that follows the copies; the weights' boxes come by TMA
 // and add one arrival.  The MMA thread makes the copies visible to the tensor core.
+//
+// The tensor core adds to its fp32 accumulators with truncation, an error that grows with
+// the number of additions (128 K values of bf16 were off by 2e-6, fp32 sums by 3e-7), so a
+// chain of kChain steps (32 MMAs) ends in a drain: the load warps add the accumulators to
+// registers, rounding to nearest, while the next chain runs in the other set of columns
+// (`sets` of them; with one the next chain waits).
+constexpr int kChain = 8;
+
 template <int NS>
 struct Ring {
-    uint64_t full[NS], empty[NS], done;
+    uint64_t full[NS], empty[NS], chain[2], drained[2];
     __device__ void init()
     {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], kWorkers + 1);
             mbar_init(&empty[i], 1);
         }
-        mbar_init(&done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&chain[i], 1);
+            mbar_init(&drained[i], kWorkers / 32);
+        }
         fence_mbar_init();
     }
 };
 
-// Load loop of one thread: copy(stage, i) starts the copies of step i.
-template <int NS, typename F>
-__device__ __forceinline__ void ring_load(Ring<NS> &r, int steps, int *status, F &&copy)
+// Load loop of one thread: copy(stage, i) starts the copies of step i, add(set) adds the
+// accumulators of a complete chain.
+template <int NS, typename F, typename G>
+__device__ __forceinline__ void ring_load(Ring<NS> &r, int steps, int sets, int *status, F &&copy, G &&add)
 {
-    for (int i = 0; i < steps; ++i) {
-        bool ok = true;
+    bool ok = true;
+    auto drain = [&](int g) {
+        const int set = g & (sets - 1);
+        ok = ok && mbar_wait(&r.chain[set], (g >> (sets - 1)) & 1, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        tc_after();
+        add(set);
+        tc_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&r.drained[set]);
+    };
+    int g = 0;
+    for (int i = 0; i < steps && ok; ++i) {
         if (i >= NS) ok = mbar_wait(&r.empty[i % NS], ((i / NS) & 1) ^ 1, status);
-        if (!__all_sync(0xffffffffu, ok)) break;
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
         copy(i % NS, i);
         cp_async_arrive(&r.full[i % NS]);
+        if (i == (g + 1) * kChain + NS - 1) drain(g++);   // (its MMAs are complete: the stage is free)
     }
+    for (; g * kChain < steps && ok; ++g) drain(g);
+    cp_async_wait<0>();
 }
 
-// Issue loop of the MMA thread: mma(stage, i) issues the MMAs of step i.
+// Issue loop of the MMA thread: mma(stage, set, fresh) issues the MMAs of a step, the first of
+// them overwriting the accumulators if fresh.
 template <int NS, typename F>
-__device__ __forceinline__ void ring_mma(Ring<NS> &r, int steps, int *status, F &&mma)
+__device__ __forceinline__ void ring_mma(Ring<NS> &r, int steps, int sets, int *status, F &&mma)
 {
     for (int i = 0; i < steps; ++i) {
+        const int g = i / kChain, set = g & (sets - 1);
+        const bool fresh = i % kChain == 0;
+        if (fresh && g >= sets && !mbar_wait(&r.drained[set], ((g >> (sets - 1)) & 1) ^ 1, status)) return;
         if (!mbar_wait(&r.full[i % NS], (i / NS) & 1, status)) return;
         fence_async_smem();
         tc_after();
-        mma(i % NS, i);
+        mma(i % NS, set, fresh);
         tc_commit(&r.empty[i % NS]);
+        if (i % kChain == kChain - 1 || i == steps - 1) tc_commit(&r.chain[set]);
     }
-    tc_commit(&r.done);
 }
 
 __device__ __forceinline__ uint32_t tmem_cols(int n) { return n <= 32 ? 32u : n <= 64 ? 64u : n <= 128 ? 128u : n <= 256 ? 256u : 512u; }
@@ -424,8 +456,8 @@ __host__ __device__ inline int shrink_w_bytes(bool grad, int R, int Kp)
 // parts in rank order and writes them: z (fp32), z as pieces with the row's scale, and for
 // the weight gradients the adapters' largest magnitudes (fp16) or z_in's pieces (bf16).
 // Bound by the rows of X.
-template <typename TX, bool kGrad>
-__global__ void __launch_bounds__(kTcThreads)
+template <typename TX, bool kGrad, int KC>   // ranks padded to 16 fit KC columns
+__global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     shrink_tile_kernel(const __grid_constant__ CUtensorMap map_w, const AdParams p)
 {
     extern __shared__ unsigned char raw[];
@@ -450,10 +482,8 @@ __global__ void __launch_bounds__(kTcThreads)
         return;
     }
     if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);
-    if (tid == 0) {
-        ring.init();
-    }
-    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(Kp));
+    if (tid == 0) ring.init();
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(2 * Kp));
     tc_before();
     __syncthreads();
     tc_after();
@@ -475,7 +505,10 @@ __global__ void __launch_bounds__(kTcThreads)
             live[i] = t >= 0;
             px[i] = X + (live[i] ? t * ld : 0) + c * 8;
         }
-        ring_load<kShrinkNS>(ring, steps, p.status, [&](int s, int i) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int half = warp >> 2;   // of the columns
+        float acc[KC / 2] = {};
+        ring_load<kShrinkNS>(ring, steps, 2, p.status, [&](int s, int i) {
             const int k0 = (b_lo + i) * 64;
             const uint32_t xs = sbuf + s * stage, ws = xs + kBlk;
             if (tid == 0) {
@@ -491,30 +524,31 @@ __global__ void __launch_bounds__(kTcThreads)
 #pragma unroll
             for (int u = 0; u < 4; ++u)
                 cp_async16_or_zero(xs + swz(r0 + 32 * u, c), live[u] && in ? px[u] + k0 : X, live[u] && in);
+        }, [&](int set) {
+#pragma unroll
+            for (int b = 0; b < KC / 2; b += 8) {
+                if (b >= Kp / 2) break;
+                float v[8];
+                tc_ld(tmem + lanes + set * Kp + half * (Kp / 2) + b, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[b + e] += v[e];
+            }
         });
-        mbar_wait(&ring.done, 0, p.status);
-        cp_async_wait<0>();
-        __syncwarp();
-        tc_after();
-        float *P = reinterpret_cast<float *>(buf);
-        const int row = (warp & 3) * 32 + lane, half = warp >> 2;
-        for (int col = half * (Kp / 2); col < (half + 1) * (Kp / 2); col += 8) {
-            float v[8];
-            tc_ld(tmem + ((uint32_t)((warp & 3) * 32) << 16) + col, v);
-            tc_wait_ld();
-            float4 *dst = reinterpret_cast<float4 *>(P + row * pitch + col);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        float *P = reinterpret_cast<float *>(buf) + ((warp & 3) * 32 + lane) * pitch + half * (Kp / 2);
+#pragma unroll
+        for (int b = 0; b < KC / 2; b += 4) {
+            if (b >= Kp / 2) break;
+            *reinterpret_cast<float4 *>(P + b) = make_float4(acc[b], acc[b + 1], acc[b + 2], acc[b + 3]);
         }
-        tc_before();
     } else if (lane == 0) {
         const uint32_t idesc = idesc16<TX>(Kp, false, kGrad);
-        ring_mma<kShrinkNS>(ring, steps, p.status, [&](int s, int i) {
+        ring_mma<kShrinkNS>(ring, steps, 2, p.status, [&](int s, int set, bool fresh) {
             const uint32_t xs = sbuf + s * stage, ws = xs + kBlk;
             const uint64_t da = sdesc_k(xs), db = kGrad ? sdesc_mn(ws, 8192) : sdesc_k(ws);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-                tc_mma16(tmem, da + 2 * kk, db + (kGrad ? 128 : 2) * kk, idesc, i > 0 || kk > 0);
+                tc_mma16(tmem + set * Kp, da + 2 * kk, db + (kGrad ? 128 : 2) * kk, idesc, !fresh || kk > 0);
         });
     }
     __syncwarp();
@@ -522,30 +556,32 @@ __global__ void __launch_bounds__(kTcThreads)
     else __syncthreads();
     if (warp == kMmaWarp) {
         tc_after();
-        tc_dealloc(tmem, tmem_cols(Kp));
+        tc_dealloc(tmem, tmem_cols(2 * Kp));
     } else if (warp < kMmaWarp) {
-        const int per = kTile / S;
         const float scaling = kGrad ? __ldcg(p.scaling + bin) : 1.f;
         const float apply_scale = kGrad ? 1.f : __ldcg(p.scaling + bin);
-#pragma unroll 2
-        for (int r = q * per + warp; r < (q + 1) * per; r += kWorkers / 32) {
+        constexpr int NI = KC / 32;   // columns of a lane
+        // one row: lanes over columns
+        auto sum = [&](int r, float (&v)[NI]) {
+#pragma unroll
+            for (int i = 0; i < NI; ++i) {
+                const int col = lane + 32 * i;
+                const uint32_t at = sbuf + (uint32_t)(r * pitch + col) * 4;
+                float part[kMaxSplit];
+#pragma unroll
+                for (int c = 0; c < kMaxSplit; ++c) part[c] = col < Kp && c < S ? ld_cluster(peer_addr(at, c)) : 0.f;
+                v[i] = 0.f;
+#pragma unroll
+                for (int c = 0; c < kMaxSplit; ++c) v[i] += part[c];
+            }
+        };
+        auto finish = [&](int r, float (&v)[NI]) {
             const int tok = s_tok[r];
             const size_t pos = (size_t)tile * kTile + r;
-            float v[4], m = 0.f;
+            float m = 0.f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int col = lane + 32 * i;
-                v[i] = 0.f;
-                if (col < Kp) {
-                    const uint32_t at = sbuf + (uint32_t)(r * pitch + col) * 4;
-                    float part[kMaxSplit];
-#pragma unroll
-                    for (int c = 0; c < kMaxSplit; ++c) part[c] = c < S ? ld_cluster(peer_addr(at, c)) : 0.f;
-#pragma unroll
-                    for (int c = 0; c < kMaxSplit; ++c) v[i] += part[c];
-                    if (col >= rank || tok < 0) v[i] = 0.f;   // (what lies past the rank is not used)
-                    v[i] *= scaling;
-                }
+            for (int i = 0; i < NI; ++i) {
+                v[i] = lane + 32 * i < rank && tok >= 0 ? v[i] * scaling : 0.f;   // (what lies past the rank is not used)
                 m = fmaxf(m, finite_or_0(v[i]));
             }
             m = warp_max(m);
@@ -553,7 +589,7 @@ __global__ void __launch_bounds__(kTcThreads)
             const float c = norm_scale(m, inv);
             TX *pieces = static_cast<TX *>(p.pieces) + pos * kPieces<TX> * Kp;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < NI; ++i) {
                 const int col = lane + 32 * i;
                 if (col >= Kp) continue;
                 store_pieces(v[i] * (TcType<TX>::code ? 1.f : c), pieces + col, Kp);   // (bf16 has fp32's range)
@@ -565,7 +601,7 @@ __global__ void __launch_bounds__(kTcThreads)
                 float zm = 0.f;
                 TX *zl = static_cast<TX *>(p.zl) + pos * kPieces<TX> * Kp;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < NI; ++i) {
                     const int col = lane + 32 * i;
                     const float z = col < rank && tok >= 0 ? __ldcg(p.z_in + (size_t)tok * R + col) : 0.f;
                     if (TcType<TX>::code) {
@@ -582,10 +618,28 @@ __global__ void __launch_bounds__(kTcThreads)
                     }
                 }
             }
+        };
+        if (S == kMaxSplit) {   // two rows a warp: both read, then the peers are free
+            float v[2][NI];
+            sum(q * 16 + warp, v[0]);
+            sum(q * 16 + 8 + warp, v[1]);
+            cluster_done_reading();
+            finish(q * 16 + warp, v[0]);
+            finish(q * 16 + 8 + warp, v[1]);
+        } else {
+            const int per = kTile / S;
+            for (int r = q * per + warp; r < (q + 1) * per; r += kWorkers / 32) {
+                float v[NI];
+                sum(r, v);
+                finish(r, v);
+            }
+            if (S > 1) cluster_done_reading();
         }
     }
-    __syncwarp();
-    if (S > 1) cluster_sync();   // no CTA leaves while a peer reads its sums
+    if (S > 1) {
+        if (warp == kMmaWarp) cluster_done_reading();
+        cluster_wait_readers();   // no CTA leaves while a peer reads its sums
+    }
 }
 
 // fp16 pools: dz and z as pieces under one scale per adapter (a sum over tokens has no
@@ -616,13 +670,15 @@ __global__ void __launch_bounds__(kWorkers) pieces_kernel(const AdParams p)
 // da[a][j][k] = sum_t dz[t][j] x[t][k] and db[a][n][j] = s sum_t z[t][j] dy[t][n]: one product
 // D[c][j] = sum_t X[t][c] Z[t][j] over an adapter's tokens, 128 columns c of X per cluster,
 // its tokens dealt to the S CTAs 64 at a time.  Both operands are MN-major (rows are
-// tokens); Z's pieces lie side by side as the columns
-// of one MMA (two MMAs past 256 columns).  The CTAs' parts meet
-// as in the shrink kernel.  Bound by reading X.
+// tokens); Z's pieces lie side by side as the columns of one
+// MMA (two MMAs past 256 columns).  The CTAs' parts meet as in the shrink kernel.  Bound by reading X.
 __host__ __device__ inline int grad_z_bytes(int cols) { return (cols + 63) / 64 * 8192; }
 
-template <typename TX, int NS>
-__global__ void __launch_bounds__(kTcThreads)
+// accumulator sets: two where two CTAs of an SM can hold them
+__host__ __device__ inline int grad_sets(int cols) { return 2 * cols <= 256 ? 2 : 1; }
+
+template <typename TX, int KC, int NS>
+__global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     grad_tile_kernel(const __grid_constant__ CUtensorMap map_dz, const __grid_constant__ CUtensorMap map_z,
                      const AdParams p)
 {
@@ -652,10 +708,9 @@ __global__ void __launch_bounds__(kTcThreads)
         return;
     }
     const size_t pos0 = (size_t)__ldcg(p.seg + a);
-    if (tid == 0) {
-        ring.init();
-    }
-    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(ZC));
+    const int sets = grad_sets(ZC);
+    if (tid == 0) ring.init();
+    if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(sets * ZC));
     tc_before();
     __syncthreads();
     tc_after();
@@ -677,7 +732,10 @@ __global__ void __launch_bounds__(kTcThreads)
             return step < steps ? __ldcg(p.entry_of + pos0 + (size_t)(q + step * S) * 64 + row) : -1;
         };
         int ids = tokens(0), next = tokens(4);
-        ring_load<NS>(ring, steps, p.status, [&](int s, int i) {
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int half = warp >> 2;   // of the ranks
+        float acc[KC / 2] = {};
+        ring_load<NS>(ring, steps, sets, p.status, [&](int s, int i) {
             const uint32_t xs = sbuf + s * stage + (cx >> 3) * 8192, zs = sbuf + s * stage + 2 * 8192;
             if (tid == 0) {
                 mbar_arrive_expect_tx(&ring.full[s], stage - 2 * 8192);
@@ -694,40 +752,42 @@ __global__ void __launch_bounds__(kTcThreads)
                 const bool in = t >= 0 && in_x;
                 cp_async16_or_zero(xs + swz(rx + 16 * u, cx & 7), in ? Xc + t * ld : X, in);
             }
-        });
-        if (steps > 0) mbar_wait(&ring.done, 0, p.status);
-        cp_async_wait<0>();
-        __syncwarp();
-        tc_after();
-        const int c = (warp & 3) * 32 + lane, half = warp >> 2;
-        for (int j = half * (Kp / 2); j < (half + 1) * (Kp / 2); j += 8) {
-            float v[kPieces<TX>][8] = {};
-            if (steps > 0) {
+        }, [&](int set) {
+#pragma unroll
+            for (int b = 0; b < KC / 2; b += 8) {
+                if (b >= Kp / 2) break;
+                float v[kPieces<TX>][8];
 #pragma unroll
                 for (int l = 0; l < kPieces<TX>; ++l)
-                    tc_ld(tmem + ((uint32_t)((warp & 3) * 32) << 16) + l * Kp + j, v[l]);
+                    tc_ld(tmem + lanes + set * ZC + l * Kp + half * (Kp / 2) + b, v[l]);
                 tc_wait_ld();
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float sum = v[kPieces<TX> - 1][e];   // (the smallest first)
+                for (int e = 0; e < 8; ++e) {
+                    float sum = v[kPieces<TX> - 1][e];   // (the smallest first)
 #pragma unroll
-                for (int l = kPieces<TX> - 2; l >= 0; --l) sum += v[l][e];
-                if (is_b) P[c * pitch + j + e] = sum;
-                else P[(j + e) * pitch + c] = sum;
+                    for (int l = kPieces<TX> - 2; l >= 0; --l) sum += v[l][e];
+                    acc[b + e] += sum;
+                }
             }
+        });
+        const int c = (warp & 3) * 32 + lane;
+#pragma unroll
+        for (int b = 0; b < KC / 2; ++b) {
+            if (b >= Kp / 2) break;
+            const int j = half * (Kp / 2) + b;
+            if (is_b) P[c * pitch + j] = acc[b];
+            else P[j * pitch + c] = acc[b];
         }
-        tc_before();
     } else if (lane == 0 && steps > 0) {
         const uint32_t idesc = idesc16<TX>(min(ZC, 256), true, true), idesc2 = idesc16<TX>(ZC - 256, true, true);
-        ring_mma<NS>(ring, steps, p.status, [&](int s, int i) {
-            const uint32_t xs = sbuf + s * stage;
+        ring_mma<NS>(ring, steps, sets, p.status, [&](int s, int set, bool fresh) {
+            const uint32_t xs = sbuf + s * stage, d = tmem + set * ZC;
             const uint64_t da = sdesc_mn(xs, 8192), db = sdesc_mn(xs + 2 * 8192, 8192);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk) {
-                tc_mma16(tmem, da + 128 * kk, db + 128 * kk, idesc, i > 0 || kk > 0);
+                tc_mma16(d, da + 128 * kk, db + 128 * kk, idesc, !fresh || kk > 0);
                 if (ZC > 256)   // (columns 256 .. start at block 4)
-                    tc_mma16(tmem + 256, da + 128 * kk, db + 4 * 512 + 128 * kk, idesc2, i > 0 || kk > 0);
+                    tc_mma16(d + 256, da + 128 * kk, db + 4 * 512 + 128 * kk, idesc2, !fresh || kk > 0);
             }
         });
     }
@@ -736,7 +796,7 @@ __global__ void __launch_bounds__(kTcThreads)
     else __syncthreads();
     if (warp == kMmaWarp) {
         tc_after();
-        tc_dealloc(tmem, tmem_cols(ZC));
+        tc_dealloc(tmem, tmem_cols(sets * ZC));
     } else if (warp < kMmaWarp) {
         float scale = is_b ? __ldcg(p.scaling + a) : 1.f, inv = 1.f;
         if (!TcType<TX>::code) {
@@ -1516,8 +1576,11 @@ cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, h->num_sms);
     const size_t ring = (size_t)kShrinkNS * (kBlk + shrink_w_bytes(kGrad, p.R, p.Kp));
     const size_t sums = (size_t)kTile * (p.Kp + 4) * 4;
-    return launch_chained(shrink_tile_kernel<TX, kGrad>, {dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s},
-                          kGrad ? h->map_b64 : h->map_a, p);
+    const ChainLaunch l = {dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s};
+    const auto kernel = p.Kp <= 32   ? shrink_tile_kernel<TX, kGrad, 32>
+                        : p.Kp <= 64 ? shrink_tile_kernel<TX, kGrad, 64>
+                                     : shrink_tile_kernel<TX, kGrad, 128>;
+    return launch_chained(kernel, l, kGrad ? h->map_b64 : h->map_a, p);
 }
 
 template <typename TX>
@@ -1527,12 +1590,16 @@ cudaError_t run_grad(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     if (p.T && !(make_pieces_map(h, &dz, p.dl, p.T) && make_pieces_map(h, &z, p.zl, p.T))) return cudaErrorInvalidValue;
     const int tiles = (p.K + 127) / 128 + (p.N + 127) / 128, live = std::max(1, std::min(p.n, p.T));
     const int S = split_of((long long)tiles * live, (p.T / live + 63) / 64, h->num_sms);
-    // four stages of 64 tokens where they fit, three for bf16 ranks above 85
+    // stages of 64 tokens: as many as let two CTAs share an SM, or three (ranks above 64)
     const size_t stage = 2 * 8192 + grad_z_bytes(kPieces<TX> * p.Kp);
     const size_t sums = (size_t)std::max(128 * (p.Kp + 4), p.Kp * 132) * 4;
-    const bool four = 4 * stage <= kMaxSmem;
-    const ChainLaunch l = {dim3(tiles * S, p.n), kTcThreads, 1024 + std::max((four ? 4 : 3) * stage, sums), S, s};
-    return launch_chained(four ? grad_tile_kernel<TX, 4> : grad_tile_kernel<TX, 3>, l, dz, z, p);
+    const int ns = p.Kp > 64 || 3 * stage <= 108 * 1024 ? 3 : 2;
+    const ChainLaunch l = {dim3(tiles * S, p.n), kTcThreads, 1024 + std::max(ns * stage, sums), S, s};
+    const auto kernel = p.Kp <= 32   ? grad_tile_kernel<TX, 32, 3>
+                        : p.Kp > 64  ? grad_tile_kernel<TX, 128, 3>
+                        : ns == 3    ? grad_tile_kernel<TX, 64, 3>
+                                     : grad_tile_kernel<TX, 64, 2>;
+    return launch_chained(kernel, l, dz, z, p);
 }
 
 template <typename TX, typename TY, bool kGrad>
@@ -1616,10 +1683,20 @@ cudaError_t prepare_expand()
 template <typename TX>
 cudaError_t prepare()
 {
-    cudaError_t e = allow_smem(shrink_tile_kernel<TX, false>);
-    if (e == cudaSuccess) e = allow_smem(shrink_tile_kernel<TX, true>);
-    if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 3>);
-    if (e == cudaSuccess) e = allow_smem(grad_tile_kernel<TX, 4>);
+    cudaError_t e = cudaSuccess;
+    auto allow = [&](auto kernel) {
+        if (e == cudaSuccess) e = allow_smem(kernel);
+    };
+    allow(shrink_tile_kernel<TX, false, 32>);
+    allow(shrink_tile_kernel<TX, false, 64>);
+    allow(shrink_tile_kernel<TX, false, 128>);
+    allow(shrink_tile_kernel<TX, true, 32>);
+    allow(shrink_tile_kernel<TX, true, 64>);
+    allow(shrink_tile_kernel<TX, true, 128>);
+    allow(grad_tile_kernel<TX, 32, 3>);
+    allow(grad_tile_kernel<TX, 64, 2>);
+    allow(grad_tile_kernel<TX, 64, 3>);
+    allow(grad_tile_kernel<TX, 128, 3>);
     if (e == cudaSuccess) e = prepare_expand<TX, __half>();
     if (e == cudaSuccess) e = prepare_expand<TX, __nv_bfloat16>();
     return e == cudaSuccess ? prepare_expand<TX, float>() : e;

@@ -149,6 +149,11 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// the same in two halves, ordering nothing: keeps a CTA's shared memory alive until every
+// peer has read it
+__device__ __forceinline__ void cluster_done_reading() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_readers() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // shared-memory address of `peer`'s copy of a local shared address
 __device__ __forceinline__ uint32_t peer_addr(uint32_t addr, uint32_t peer)
 {
