@@ -469,10 +469,11 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
     pdl_trigger();
+    const int32_t *entry = p.entry_of + (size_t)tile * kTile;
     const int bin = __ldcg(p.tile_bin + tile);
+    if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);   // (the tile is inside the plan's arrays)
     if (bin < 0) return;   // (the whole cluster)
     const int rank = rank_of(p, bin), R = p.R, Kp = p.Kp;
-    const int32_t *entry = p.entry_of + (size_t)tile * kTile;
     if (rank == 0) {
         if (p.z_out)
             for (int i = q * kTcThreads + tid; i < kTile * R; i += S * kTcThreads) {
@@ -481,7 +482,6 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
             }
         return;
     }
-    if (tid < kTile) s_tok[tid] = __ldcg(entry + tid);
     if (tid == 0) ring.init();
     if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(2 * Kp));
     tc_before();
@@ -693,8 +693,10 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
     pdl_trigger();
-    const int R = p.R, Kp = p.Kp, ZC = kPieces<TX> * Kp, rank = rank_of(p, a);
-    const int cnt = rank ? __ldcg(p.counts + a) : 0;
+    const int R = p.R, Kp = p.Kp, ZC = kPieces<TX> * Kp;
+    const int tokens_a = __ldcg(p.counts + a);
+    const size_t pos0 = (size_t)__ldcg(p.seg + a);
+    const int rank = rank_of(p, a), cnt = rank ? tokens_a : 0;
     float *out = is_b ? p.db + ((size_t)a * p.N + c0) * R : p.da + (size_t)a * R * p.K + c0;
     const int cols = min(128, width - c0);
     if (cnt == 0) {   // (the whole cluster)
@@ -707,7 +709,6 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
         }
         return;
     }
-    const size_t pos0 = (size_t)__ldcg(p.seg + a);
     const int sets = grad_sets(ZC);
     if (tid == 0) ring.init();
     if (warp == kMmaWarp) tc_alloc(&s_tmem, tmem_cols(sets * ZC));
@@ -771,12 +772,28 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
             }
         });
         const int c = (warp & 3) * 32 + lane;
+        if (S == 1 && !is_b) {   // a lane has a column: rows of da are coalesced as they are
+            float scale = 1.f;
+            if (!TcType<TX>::code) norm_scale(__uint_as_float(__ldcg(p.amax + a)), scale);
 #pragma unroll
-        for (int b = 0; b < KC / 2; ++b) {
-            if (b >= Kp / 2) break;
-            const int j = half * (Kp / 2) + b;
-            if (is_b) P[c * pitch + j] = acc[b];
-            else P[j * pitch + c] = acc[b];
+            for (int b = 0; b < KC / 2; ++b) {
+                const int j = half * (Kp / 2) + b;
+                if (b >= Kp / 2 || j >= R || c >= cols) break;
+                float *dst = out + (size_t)j * p.K + c;
+                if (p.accumulate) {
+                    if (j < rank) *dst += acc[b] * scale;
+                } else {
+                    *dst = j < rank ? acc[b] * scale : 0.f;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int b = 0; b < KC / 2; ++b) {
+                if (b >= Kp / 2) break;
+                const int j = half * (Kp / 2) + b;
+                if (is_b) P[c * pitch + j] = acc[b];
+                else P[j * pitch + c] = acc[b];
+            }
         }
     } else if (lane == 0 && steps > 0) {
         const uint32_t idesc = idesc16<TX>(min(ZC, 256), true, true), idesc2 = idesc16<TX>(ZC - 256, true, true);
@@ -797,7 +814,7 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     if (warp == kMmaWarp) {
         tc_after();
         tc_dealloc(tmem, tmem_cols(sets * ZC));
-    } else if (warp < kMmaWarp) {
+    } else if (warp < kMmaWarp && (S > 1 || is_b)) {
         float scale = is_b ? __ldcg(p.scaling + a) : 1.f, inv = 1.f;
         if (!TcType<TX>::code) {
             norm_scale(__uint_as_float(__ldcg(p.amax + (is_b ? p.n : 0) + a)), inv);
@@ -1554,12 +1571,13 @@ cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStr
     return launch_sort(q, s);
 }
 
-// CTAs of a cluster that share `blocks` steps of work so that `units` clusters give every SM
-// about two CTAs
-int split_of(long long units, int blocks, int num_sms)
+// CTAs of a cluster that share `blocks` steps of work so that `units` clusters make `want`
+// CTAs: two per SM, not more, as every CTA costs some 4 us beside its steps (weight gradients
+// of 4096 tokens, four adapters, 384 units: one CTA a unit 31 us, two 37, four 53)
+int split_of(long long units, int blocks, int want)
 {
     int S = 1;
-    while (S < kMaxSplit && units * S < 2 * num_sms && 2 * S <= blocks) S *= 2;
+    while (S < kMaxSplit && units * S < want && 2 * S <= blocks) S *= 2;
     return S;
 }
 
@@ -1573,7 +1591,7 @@ template <typename TX, bool kGrad>
 cudaError_t run_shrink(const moe_adapters *h, const AdParams &p, cudaStream_t s)
 {
     const int tiles = tiles_max(h->desc, p.T);
-    const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, h->num_sms);
+    const int S = split_of(tiles, ((kGrad ? p.N : p.K) + 63) / 64, 2 * h->num_sms);
     const size_t ring = (size_t)kShrinkNS * (kBlk + shrink_w_bytes(kGrad, p.R, p.Kp));
     const size_t sums = (size_t)kTile * (p.Kp + 4) * 4;
     const ChainLaunch l = {dim3(tiles * S), kTcThreads, 1024 + std::max(ring, sums), S, s};
@@ -1589,7 +1607,7 @@ cudaError_t run_grad(const moe_adapters *h, const AdParams &p, cudaStream_t s)
     CUtensorMap dz = {}, z = {};
     if (p.T && !(make_pieces_map(h, &dz, p.dl, p.T) && make_pieces_map(h, &z, p.zl, p.T))) return cudaErrorInvalidValue;
     const int tiles = (p.K + 127) / 128 + (p.N + 127) / 128, live = std::max(1, std::min(p.n, p.T));
-    const int S = split_of((long long)tiles * live, (p.T / live + 63) / 64, h->num_sms);
+    const int S = split_of((long long)tiles * live, (p.T / live + 63) / 64, 2 * h->num_sms);
     // stages of 64 tokens: as many as let two CTAs share an SM, or three (ranks above 64)
     const size_t stage = 2 * 8192 + grad_z_bytes(kPieces<TX> * p.Kp);
     const size_t sums = (size_t)std::max(128 * (p.Kp + 4), p.Kp * 132) * 4;
