@@ -49,6 +49,7 @@ constexpr int kWorkers = 256;      // load and epilogue threads of a tcgen05 CTA
 constexpr int kTcThreads = kWorkers + 32;   // and its MMA warp
 constexpr int kMmaWarp = kWorkers / 32, kTmaWarp = kMmaWarp + 1;
 constexpr size_t kMaxSmem = 224 * 1024;     // of a ring
+constexpr int kOrdered = 128;      // adapters that the sort ranks by size
 constexpr int kMaxSplit = 8;       // CTAs of a cluster that share a contraction
 
 struct AdParams {
@@ -65,6 +66,7 @@ struct AdParams {
     int T, K, N, R, Kp, n, accumulate, want_dw;
     // the plan: tokens sorted by adapter, tiles of 128 positions
     int32_t *seg, *counts, *entry_of, *tile_bin;
+    int32_t *order;              // adapters, most tokens first (NULL: as they are numbered)
     // intermediates, by position: z (dz) as pieces [kPieces][Kp], the scale that undoes theirs
     void *pieces, *zl, *dl;
     float *row_scale, *dz;
@@ -689,11 +691,12 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
     const int S = cluster_size(), q = cluster_rank();
     const int tiles_a = (p.K + 127) / 128, ct = blockIdx.x / S;
     const bool is_b = ct >= tiles_a;
-    const int c0 = (is_b ? ct - tiles_a : ct) * 128, width = is_b ? p.N : p.K, a = blockIdx.y;
+    const int c0 = (is_b ? ct - tiles_a : ct) * 128, width = is_b ? p.N : p.K;
     unsigned char *buf = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     pdl_wait();
     pdl_trigger();
     const int R = p.R, Kp = p.Kp, ZC = kPieces<TX> * Kp;
+    const int a = p.order ? __ldcg(p.order + blockIdx.y) : blockIdx.y;   // (long units start first)
     const int tokens_a = __ldcg(p.counts + a);
     const size_t pos0 = (size_t)__ldcg(p.seg + a);
     const int rank = rank_of(p, a), cnt = rank ? tokens_a : 0;
@@ -1431,7 +1434,7 @@ int rank_pad(const moe_adapters_desc &d) { return (d.max_rank + 15) / 16 * 16; }
 
 // a call's workspace: the small path's partial sums share the bytes of the other path
 struct AdWs {
-    size_t seg, counts, entry_of, tile_bin, hist, pieces, row_scale, zl, dl, dz, amax, total;
+    size_t seg, counts, entry_of, tile_bin, order, hist, pieces, row_scale, zl, dl, dz, amax, total;
 };
 
 AdWs ad_layout(const moe_adapters_desc &d, int T)
@@ -1444,6 +1447,7 @@ AdWs ad_layout(const moe_adapters_desc &d, int T)
     w.counts = o; o = up256(o + bins * 4);
     w.entry_of = o; o = up256(o + rows * 4);
     w.tile_bin = o; o = up256(o + tiles * 4);
+    w.order = o; o = up256(o + bins * 4);
     w.hist = o; o = up256(o + ((size_t)T + kSortChunk - 1) / kSortChunk * bins * 4);
     w.pieces = o; o = up256(o + pieces);
     w.row_scale = o; o = up256(o + rows * 4);
@@ -1502,6 +1506,7 @@ AdParams ad_params(const moe_adapters *h, const int32_t *adapter_of, int T, void
     p.counts = reinterpret_cast<int32_t *>(at(w.counts));
     p.entry_of = reinterpret_cast<int32_t *>(at(w.entry_of));
     p.tile_bin = reinterpret_cast<int32_t *>(at(w.tile_bin));
+    p.order = d.n_adapters <= kOrdered ? reinterpret_cast<int32_t *>(at(w.order)) : nullptr;
     p.pieces = at(w.pieces);
     p.row_scale = reinterpret_cast<float *>(at(w.row_scale));
     p.zl = at(w.zl);
@@ -1563,6 +1568,7 @@ cudaError_t run_sort(const moe_adapters *h, const AdParams &p, void *ws, cudaStr
     q.seg = p.seg;
     q.entry_of = p.entry_of;
     q.tile_bin = p.tile_bin;
+    q.order = p.want_dw ? p.order : nullptr;
     q.max_tiles = tiles_max(h->desc, p.T);
     q.zero = p.amax;
     q.n_zero = 2 * p.n;

@@ -140,6 +140,7 @@ struct SortParams {
     int32_t *entry_of;    // optional: entry at each position, -1 in the padding of a group
     int32_t *tile_bin;    // optional [max_tiles]: bin of each `align` positions, -1 behind the last
     int max_tiles;
+    int32_t *order;       // optional [E - 1]: the bins but the last, largest first (E <= 129)
     unsigned *zero;       // optional: n_zero words to clear
     int n_zero;
     int32_t *hist;        // scratch [ceil(n / kSortChunk)][E] (unused when n <= kSortChunk)

@@ -170,6 +170,11 @@ __global__ void __launch_bounds__(kSortThreads) sort_place_kernel(SortParams p)
     }
     if (chunk == 0) {
         for (int i = tid; i < p.n_zero; i += kSortThreads) p.zero[i] = 0u;
+        if (p.order && tid < p.E - 1) {
+            int at = 0;
+            for (int e = 0; e < p.E - 1; ++e) at += all[e] > all[tid] || (all[e] == all[tid] && e < tid);
+            p.order[at] = tid;
+        }
         if (p.tile_bin) {
             for (int e = tid; e < p.E; e += kSortThreads)
                 for (int i = seg[e] / p.align; i < seg[e + 1] / p.align; ++i) p.tile_bin[i] = e;
