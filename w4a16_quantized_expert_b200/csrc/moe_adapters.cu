@@ -1029,7 +1029,25 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
     } else if (warp == kEpiWarps + 2) {
         // ---- a last K step that the rank does not fill: what lies past the rank becomes zero
         // (the step's z is zero there, but a NaN or an infinity would still spoil the sum)
+        // ---- and the y_in of the items two ahead of the epilogue's loads into L2
+        int f_it = lo, f_lt = 0, f_nt = lo - tile0 * nt_all;
+        auto prefetch = [&] {
+            if (!in || f_it >= hi) return;
+            const int n = f_nt * NW;
+#pragma unroll
+            for (int r = 0; r < kTile; r += 32) {
+                const int t = s_tok[f_lt * kTile + r + lane];
+                if (t < 0) continue;
+                const TY *row = in + t * p.ldy_in + n;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(row));
+                if (n + NB < width) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + NB));
+            }
+            ++f_it;
+            if (++f_nt == nt_all) f_nt = 0, ++f_lt;
+        };
+        for (int i = 0; i < 6; ++i) prefetch();
         for (int it = lo; it < hi; ++it) {
+            prefetch();
             const int rank = s_rank[it / nt_all - tile0];
             if (!rank) continue;
             const bool ok = mbar_wait(&wland[s], ph, p.status);
