@@ -467,3 +467,88 @@ def test_adapters_and_sorted_rows_in_the_staged_layer(T):
     near(dw, prod.sum(2), (H // 32 + 16) * ULP * prod.abs().sum(2), "dw")
     assert moe.moe_get_device_status(L.handle) == moe.MOE_OK
     assert on_router.h.status() == on_shared.h.status() == moe.MOE_OK
+
+
+def test_no_token_with_an_input_gradient():
+    P = Pool(64, 16, 3, 8, "f16", 4)
+    ws = P.h.workspace(0)
+    dx = torch.empty((1, 64), dtype=torch.float16, device="cuda")
+    da, db = torch.full((3, 8, 64), 5.0, device="cuda"), torch.full((3, 16, 8), 5.0, device="cuda")
+    moe.moe_adapters_backward(P.h.handle, None, 0, None, None, 0, None, 0, None, 0, dx.data_ptr(), 0, 64,
+                              da.data_ptr(), db.data_ptr(), 0, ws.data_ptr(), ws.numel())
+    assert not da.any() and not db.any()
+
+
+@pytest.mark.parametrize("T,K,N,n,R,kind", [
+    (20000, 64, 64, 1024, 8, "each"),      # more chunks than a cluster sorts, more adapters than are ranked
+    (3000, 4096, 128, 2, 128, "one"),      # one adapter, long chains of both kinds, the widest rank
+    (4097, 128, 2048, 130, 24, "runs"),
+])
+@pytest.mark.parametrize("xt", ["f16", "bf16"])
+def test_large_batches(T, K, N, n, R, kind, xt):
+    P = Pool(K, N, n, R, xt, T, seed=1)
+    which = assign(T, n, 1, kind)
+    run_apply(P, which, xt, "f32", 7)
+    x, dy = rand((T, K), DT[xt], 1), rand((T, N), DT[xt], 2)
+    z = rand((T, R), torch.float32, 3)
+    da, db = torch.empty((n, R, K), device="cuda"), torch.empty((n, N, R), device="cuda")
+    dx = torch.empty((T, K), device="cuda")
+    P.h.backward(x, z, dy, which, P.ws, dx=dx, da=da, db=db)
+    check_backward(P, x, z, dy, which, None, dx, da, db)
+    assert P.h.status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T", [20, 2100])
+def test_offsets_past_32_bits(T):
+    """Rows 2^21 elements apart: the last ones lie more than 2^32 elements behind the first
+    (for the larger batch)."""
+    K, N, n, R = 64, 72, 3, 16
+    ld = 2 ** 21 if T > 32 else 2 ** 27
+    P = Pool(K, N, n, R, "f16", T)
+    which = assign(T, n, 1, "each")
+    buf = torch.empty((T, ld), dtype=torch.float16, device="cuda")
+    x, y = buf[:, :K], buf[:, K:K + N]
+    x.copy_(rand((T, K), torch.float16, 1))
+    y_in = rand((T, N), torch.float16, 2)
+    y.copy_(y_in)
+    z = torch.empty((T, R), device="cuda")
+    P.h.apply(x, which, P.ws, y_in=y, y=y, z=z)
+    check_apply(P, x, which, y, y_in, z)
+    dx = buf[:, 256:256 + K]
+    da, db = torch.empty((n, R, K), device="cuda"), torch.empty((n, N, R), device="cuda")
+    dy = buf[:, 512:512 + N]
+    dy.copy_(rand((T, N), torch.float16, 3))
+    P.h.backward(x, z, dy, which, P.ws, dx=dx, da=da, db=db)
+    check_backward(P, x, z, dy, which, None, dx, da, db)
+    assert P.h.status() == moe.MOE_OK
+
+
+def test_two_streams_at_once():
+    """Calls of one handle on two streams, each with a workspace of its own."""
+    T, K, N, n, R = 600, 512, 256, 4, 32
+    P = Pool(K, N, n, R, "bf16", T)
+    which = assign(T, n, 1, "runs")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    xs = [rand((T, K), torch.bfloat16, i) for i in range(2)]
+    dys = [rand((T, N), torch.bfloat16, 5 + i) for i in range(2)]
+    wss = [P.h.workspace(T) for _ in range(2)]
+    outs = [[torch.empty((T, N), dtype=torch.bfloat16, device="cuda"), torch.empty((T, R), device="cuda"),
+             torch.empty((T, K), dtype=torch.bfloat16, device="cuda"), torch.empty((n, R, K), device="cuda"),
+             torch.empty((n, N, R), device="cuda")] for _ in range(3)]
+
+    def step(i, o, ws):
+        P.h.apply(xs[i], which, ws, y=o[0], z=o[1])
+        P.h.backward(xs[i], o[1], dys[i], which, ws, dx=o[2], da=o[3], db=o[4])
+
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                step(i, outs[i], wss[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        step(i, outs[2], P.ws)
+        torch.cuda.synchronize()
+        for a, b in zip(outs[i], outs[2]):
+            assert torch.equal(a, b)
+    assert P.h.status() == moe.MOE_OK

@@ -402,3 +402,68 @@ def test_captured_and_replayed_on_another_stream():
         for a, b in zip(got, (y, dx, grads[1], out[1])):
             assert torch.equal(a, b)
     assert status(L) == moe.MOE_OK
+
+
+def test_offsets_past_32_bits():
+    """Sorted rows of more than 2^31 elements: every token comes back from its eight copies.
+    (Eight times an eighth of a value, summed in fp32, is the value itself; of the zeros, -0 comes
+    back as +0, as a sum that starts at +0 does: +0 + -0 = +0.)"""
+    T, H, E, k = 44000, 6144, 64, 8
+    L = layer(H, E, k, T)
+    x = rand((T, H), torch.float16, 1)
+    idx = torch.randint(0, E - k + 1, (T, 1), device="cuda", dtype=torch.int32) + \
+        torch.arange(k, device="cuda", dtype=torch.int32)
+    rows, row_of, counts, seg = L.sort_tokens(x, idx, L.sort_workspace(T))
+    assert rows.numel() > 2 ** 31 and int(seg[-1]) == T * k
+    assert torch.equal(torch.sort(row_of.reshape(-1))[0], torch.arange(T * k, device="cuda", dtype=torch.int32))
+    w = torch.full((T, k), 0.125, device="cuda")
+    y = L.unsort_tokens(rows, row_of, w)
+    assert torch.equal(y, x)
+    drows, dw = L.unsort_tokens_backward(x, rows, row_of, w)
+    last = row_of[-1].long()
+    assert torch.equal(bits(drows[last]), bits((x[-1].float() * 0.125).half().expand(k, H)))
+    norm = (x.double() ** 2).sum(1, keepdim=True).expand(T, k)
+    near(dw, norm, norm, H // 32 + 16, "dw")
+    dx = L.sort_tokens_backward(drows, row_of)
+    exact = drows[row_of.long()[-1000:]].double().sum(1)
+    near(dx[-1000:], exact, exact.abs(), k, "dx")
+    assert status(L) == moe.MOE_OK
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 256, 8), (65, 256, 8), (256, 16, 8), (257, 16, 8), (2048, 256, 8),
+                                   (2049, 256, 8)])
+def test_sort_at_the_borders_of_its_paths(T, E, k):
+    """512 assignments (one launch), 2048 (one chunk) and 16384 (one cluster), and one token more."""
+    H, align = 64, 4
+    L = layer(H, E, k, T)
+    idx = routing(T, E, k, T)
+    x = rand((T, H), torch.bfloat16, 1)
+    rows, row_of, counts, seg = L.sort_tokens(x, torch.from_numpy(idx).cuda(), L.sort_workspace(T), align=align)
+    want = sorted_by_hand(idx, E, align)
+    for g, w in zip((row_of, counts, seg), want):
+        assert np.array_equal(g.cpu().numpy(), w)
+    a = torch.from_numpy(np.flatnonzero(want[0].reshape(-1) >= 0)).cuda()
+    assert torch.equal(bits(rows[row_of.reshape(-1)[a].long()]), bits(x[a // k]))
+
+
+def test_two_streams_at_once():
+    """Calls of one handle on two streams, each with a workspace of its own."""
+    T, H, E, k = 700, 512, 32, 4
+    L = layer(H, E, k, T)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    xs = [rand((T, H), torch.float16, i) for i in range(2)]
+    ids = [torch.from_numpy(routing(T, E, k, i)).cuda() for i in range(2)]
+    wss = [L.sort_workspace(T) for _ in range(2)]
+    torch.cuda.synchronize()
+    outs = [None, None]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i] = L.sort_tokens(xs[i], ids[i], wss[i], out=outs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        row_of, counts, seg = sorted_by_hand(ids[i].cpu().numpy(), E, 1)
+        assert np.array_equal(outs[i][1].cpu().numpy(), row_of)
+        a = torch.from_numpy(np.flatnonzero(row_of.reshape(-1) >= 0)).cuda()
+        assert torch.equal(bits(outs[i][0][outs[i][1].reshape(-1)[a].long()]), bits(xs[i][a // k]))
+    assert status(L) == moe.MOE_OK

@@ -868,7 +868,7 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
 // buffered.  Sixteen epilogue warps (32 tokens x 128 bytes of every second item) turn D's
 // rows (a TMEM lane is a token) into coalesced rows through shared memory and add y_in,
 // whose loads run an item ahead, 64 KB per SM.  Bound by reading y_in and writing y.  Measured for
-// 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): EXPAND_US us;
+// 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): 31 us;
 // a lane per token straight to memory 67 us and a lane per column 44 us (the load/store
 // unit), TMA row gathers and scatters 62 us (about 75 cycles per four rows).
 constexpr int kEpiWarps = 16;
@@ -1761,7 +1761,7 @@ cudaError_t run_backward(const moe_adapters *h, const AdParams &p, int dx_dtype,
     if (e == cudaSuccess && p.want_dw && p.T && !TcType<TX>::code)
         e = launch_chained(pieces_kernel, {dim3(tiles_max(h->desc, p.T) * (kTile / (kWorkers / 32))), kWorkers, 0, 1, s}, p);
     if (e == cudaSuccess && p.want_dw) e = run_grad<TX>(h, p, s);
-    return e != cudaSuccess || !p.y ? e : run_expand<TX, true>(h, p, dx_dtype, s);
+    return e != cudaSuccess || !p.y || !p.T ? e : run_expand<TX, true>(h, p, dx_dtype, s);
 }
 
 }  // namespace

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kRowThreads) sort_copy_kernel(CopyParams p)
 // The sort and the copy of a decode-sized batch (at most kSmallSort assignments) in one
 // launch: every CTA counts all the keys itself (a few per thread), scans the counts and ranks
 // its own token's assignments, so that nothing waits for another CTA.  One token of 6144
-// fp16 and 8 of 256 experts: SMALL_US us a call in a graph, two launches 4.3.
+// fp16 and 8 of 256 experts: 3.6 us a call in a graph, two launches 4.3.
 constexpr int kSmallSort = 512;
 
 __global__ void __launch_bounds__(kRowThreads) sort_small_kernel(SortParams s, CopyParams p)
