@@ -866,13 +866,16 @@ __global__ void __launch_bounds__(kTcThreads, KC <= 64 ? 2 : 1)
 // Operands: z's pieces [128 tokens][pieces x Kp] K-major, loaded once per tile; B [columns]
 // [ranks] K-major, or A [ranks][columns] MN-major, in a ring; both by TMA; D in TMEM, double
 // buffered.  Sixteen epilogue warps (32 tokens x 128 bytes of every second item) turn D's
-// rows (a TMEM lane is a token) into coalesced rows through shared memory and add y_in,
-// whose loads run an item ahead, 64 KB per SM.  Bound by reading y_in and writing y.  Measured for
-// 4096 tokens of 6144 bf16 columns, rank 64 (16 us of traffic at the copy peak): 31 us;
-// a lane per token straight to memory 67 us and a lane per column 44 us (the load/store
-// unit), TMA row gathers and scatters 62 us (about 75 cycles per four rows).
+// rows (a TMEM lane is a token) into whole 128-byte pieces of rows through shared memory and
+// add y_in, whose loads run an item ahead, 64 KB per SM, and its lines two items ahead of
+// those into L2.  Bound by reading y_in and writing y.  Measured for 4096 tokens of 6144 bf16
+// columns, rank 64 (100 MB: 16 us at the copy peak, 21 us for a bare read-add-write kernel of
+// that size): 30 us; earlier forms: a lane per token straight to memory 67 us and a lane per
+// column 44 us (the load/store unit), TMA row gathers and scatters 62 us (about 75 cycles per
+// four rows), eight epilogue warps 34 us (latency).
 constexpr int kEpiWarps = 16;
 constexpr int kExpandThreads = kEpiWarps * 32 + 96;   // epilogue, MMA, TMA, fix warps
+constexpr int kScratch = 4608;                      // bytes of an epilogue warp's block: 32 x 36 or 16 x 68 floats
 constexpr int kAnyThreads = kWorkers + 96;
 constexpr int kExpandNS = 4;                    // weight stages at most
 constexpr int kAnyNS = 3;
@@ -1093,11 +1096,12 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         // ---- epilogue: tokens [32 q4, +32), 128 bytes of columns of every second item with a
         // product (and of the others), so that sixteen warps hide one another's latencies
         const int q4 = warp & 3, half = (warp >> 2) & 1, group = warp >> 3;
-        constexpr int kPitch = 36;                        // floats of a row of the warp's block
-        float *sc = reinterpret_cast<float *>(buf + zb + ns * wb) + warp * 32 * kPitch;
-        constexpr int CE = 16 / sizeof(TY), LPR = 32 / CE, RPA = 32 / LPR;   // a lane's 16 bytes, lanes of a row, rows
-        constexpr int NP = NB / 32, NA = LPR;             // passes of 32 columns, accesses of a pass
-        const int rl = lane / LPR, cl = half * NB + lane % LPR * CE;
+        constexpr int CE = 16 / sizeof(TY);               // elements of a lane's access: 8 lanes, 128 bytes a row
+        constexpr int NP = NB / 32, RP = 32 / NP;         // passes, their rows
+        constexpr int NA = RP / 4;                        // accesses of a pass, four rows each
+        constexpr int kPitch = NB + 4;                    // floats of a row of the warp's block
+        float *sc = reinterpret_cast<float *>(buf + zb + ns * wb + warp * kScratch);
+        const int rl = lane >> 3, cl = half * NB + (lane & 7) * CE;
         struct Item {
             int it, lt, nt, j;
         };
@@ -1120,9 +1124,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
         };
         uint4 pre[NP][NA];
         auto fetch = [&](const Item &i, int ps, int a) {
-            const int n = i.nt * NW + cl + ps * 32;
+            const int n = i.nt * NW + cl;
             if (!in || i.it >= hi || n >= width) return;
-            const int t = s_tok[i.lt * kTile + q4 * 32 + a * RPA + rl];
+            const int t = s_tok[i.lt * kTile + q4 * 32 + ps * RP + a * 4 + rl];
             if (t >= 0) pre[ps][a] = *reinterpret_cast<const uint4 *>(in + t * p.ldy_in + n);
         };
         Item at = {lo, 0, lo - tile0 * nt_all, 0};
@@ -1150,41 +1154,45 @@ __global__ void __launch_bounds__(kExpandThreads, 1)
             for (int ps = 0; ps < NP; ++ps) {
                 if (product) {
 #pragma unroll
-                    for (int h = 0; h < 32; h += 16) {
+                    for (int h = 0; h < NB; h += 16) {
                         float v[16];
-                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + group * 128 + half * NB + ps * 32 + h, v);
+                        tc_ld(tmem + ((uint32_t)(q4 * 32) << 16) + group * 128 + half * NB + h, v);
                         tc_wait_ld();
+                        if (lane / RP == ps)   // (a 16-bit row's 128 bytes are 64 columns: 16 rows at a time)
 #pragma unroll
-                        for (int e = 0; e < 16; e += 4)
-                            *reinterpret_cast<float4 *>(sc + lane * kPitch + h + e) =
-                                make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<float4 *>(sc + (lane & (RP - 1)) * kPitch + h + e) =
+                                    make_float4(v[e] * scale, v[e + 1] * scale, v[e + 2] * scale, v[e + 3] * scale);
                     }
                     tc_before();
                     __syncwarp();
                     if (ps == NP - 1 && lane == 0) mbar_arrive(&tempty[group]);
                 }
-                const int n = at.nt * NW + cl + ps * 32;
+                const int n = at.nt * NW + cl;
 #pragma unroll
                 for (int a = 0; a < NA; ++a) {
                     uint4 o = pre[ps][a];
                     if (product) {
-                        const float *d = sc + (a * RPA + rl) * kPitch + lane % LPR * CE;
+                        const float *d = sc + (a * 4 + rl) * kPitch + (lane & 7) * CE;
                         uint32_t *f = &o.x;
-#pragma unroll
-                        for (int h = 0; h < CE / 4; ++h) {
-                            const float4 x = *reinterpret_cast<const float4 *>(d + 4 * h);
-                            if (sizeof(TY) == 4) {
-                                f[0] = add_pair<TY>(f[0], x.x, 0.f);
-                                f[1] = add_pair<TY>(f[1], x.y, 0.f);
-                                f[2] = add_pair<TY>(f[2], x.z, 0.f);
-                                f[3] = add_pair<TY>(f[3], x.w, 0.f);
-                            } else {
-                                f[2 * h] = add_pair<TY>(f[2 * h], x.x, x.y);
-                                f[2 * h + 1] = add_pair<TY>(f[2 * h + 1], x.z, x.w);
-                            }
+                        if (sizeof(TY) == 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(d);
+                            f[0] = add_pair<TY>(f[0], x.x, 0.f);
+                            f[1] = add_pair<TY>(f[1], x.y, 0.f);
+                            f[2] = add_pair<TY>(f[2], x.z, 0.f);
+                            f[3] = add_pair<TY>(f[3], x.w, 0.f);
+                        } else {   // (a row's last four lanes take their halves in turn: no bank twice)
+                            const int h = lane & 4;
+                            const float4 u = *reinterpret_cast<const float4 *>(d + h);
+                            const float4 w = *reinterpret_cast<const float4 *>(d + (h ^ 4));
+                            const float4 x = h ? w : u, z = h ? u : w;
+                            f[0] = add_pair<TY>(f[0], x.x, x.y);
+                            f[1] = add_pair<TY>(f[1], x.z, x.w);
+                            f[2] = add_pair<TY>(f[2], z.x, z.y);
+                            f[3] = add_pair<TY>(f[3], z.z, z.w);
                         }
                     }
-                    const int t = s_tok[at.lt * kTile + q4 * 32 + a * RPA + rl];
+                    const int t = s_tok[at.lt * kTile + q4 * 32 + ps * RP + a * 4 + rl];
                     if (t >= 0 && n < width && (product || in != y)) *reinterpret_cast<uint4 *>(y + t * p.ldy + n) = o;
                     fetch(next, ps, a);
                 }
@@ -1653,7 +1661,7 @@ cudaError_t run_expand_tiles(const moe_adapters *h, const AdParams &p, cudaStrea
     CUtensorMap z;
     if (width * es % 16 == 0 && rows16(p.y, p.ldy) && rows16(p.y_in, p.ldy_in) && tiles / h->num_sms + 2 <= kMaxRun) {
         if (!make_pieces_map(h, &z, p.pieces, p.T)) return cudaErrorInvalidValue;
-        const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kEpiWarps * 32 * 36 * 4;
+        const size_t wb = expand_w_bytes(kGrad, p.Kp, 256 / es), scratch = kEpiWarps * kScratch;
         const size_t fixed = 1024 + expand_z_bytes(use_pieces<TX, TY>() * p.Kp) + scratch;
         const int ns = (int)std::min<size_t>(kExpandNS, (kMaxSmem - 16 * 1024 - fixed) / wb);   // (16 KB: the run's tiles)
         return launch_chained(expand_tile_kernel<TX, TY, kGrad>, {dim3(h->num_sms), kExpandThreads, fixed + ns * wb, 1, s},
