@@ -400,7 +400,8 @@ size_t moe_adapters_workspace_size(const moe_adapters *adapters, int T);
  * (MOE_DTYPE_*), y_in of the same type (NULL: zeros; y itself: in place; otherwise it may not
  * overlap y), any element alignment.  A token without an adapter gets y_in's bits.  z, if not
  * NULL, receives A_a x[t] (fp32 [T][R], 16-byte aligned, zeros from the adapter's rank on and
- * for tokens without an adapter), which the gradient needs. */
+ * for tokens without an adapter), which the gradient needs.  No output may overlap another
+ * argument (y = y_in excepted). */
 int moe_adapters_apply(const moe_adapters *adapters, const void *x, int64_t ldx, const int32_t *adapter_of, int T,
                        const void *y_in, int64_t ldy_in, void *y, int y_dtype, int64_t ldy, float *z,
                        void *workspace, size_t workspace_bytes, moe_stream_t stream);
@@ -414,7 +415,8 @@ int moe_adapters_apply(const moe_adapters *adapters, const void *x, int64_t ldx,
  * da and db, both or neither (NULL), 16-byte aligned.  accumulate = 0: every element is
  * written, zeros where the batch has no token or from the adapter's rank on;
  * accumulate = 1: the sums are added to what is there, and adapters without a token are
- * left as they were.  y_in's gradient is dy.  T = 0 with accumulate = 0 writes zeros. */
+ * left as they were.  y_in's gradient is dy.  T = 0 with accumulate = 0 writes zeros.
+ * No output may overlap another argument (dx = dx_in excepted). */
 int moe_adapters_backward(const moe_adapters *adapters, const void *x, int64_t ldx, const float *z, const void *dy,
                           int64_t lddy, const int32_t *adapter_of, int T, const void *dx_in, int64_t lddx_in,
                           void *dx, int dx_dtype, int64_t lddx, float *da, float *db, int accumulate,

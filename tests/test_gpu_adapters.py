@@ -124,7 +124,8 @@ SHAPES = [  # T, K, N, n, R, kind
     (31, 520, 256, 1024, 8, "each"), (33, 512, 136, 5, 128, "each"), (64, 6144, 256, 16, 8, "each"),
     (100, 136, 72, 7, 72, "runs"), (129, 264, 1000, 3, 16, "one"), (200, 2048, 512, 2, 8, "runs"),
     (300, 192, 64, 1, 128, "runs"), (515, 320, 328, 9, 56, "runs"), (1000, 64, 64, 1000, 8, "each"),
-    (700, 1024, 640, 4, 32, "one"), (2100, 128, 128, 12, 64, "runs"),
+    (700, 1024, 640, 4, 32, "one"), (2100, 128, 128, 12, 64, "runs"), (70, 96, 37, 3, 16, "each"),
+    (400, 64, 257, 2, 120, "runs"),
 ]
 
 

@@ -372,11 +372,12 @@ __global__ void __launch_bounds__(kFewThreads) expand_few_kernel(const AdParams 
 // and add one arrival.  The MMA thread makes the copies visible to the tensor core.
 //
 // The tensor core adds to its fp32 accumulators with truncation, an error that grows with
-// the number of additions (128 K values of bf16 were off by 2e-6, fp32 sums by 3e-7), so a
-// chain of kChain steps (32 MMAs) ends in a drain: the load warps add the accumulators to
-// registers, rounding to nearest, while the next chain runs in the other set of columns
-// (`sets` of them; with one the next chain waits).
-constexpr int kChain = 8;
+// the number of additions (weight gradients over 1000 bf16 tokens were off by 2e-6, plain
+// fp32 sums by 9e-7), so a chain of kChain steps (16 MMAs) ends in a drain: the load warps
+// add the accumulators to registers, rounding to nearest, while the next chain runs in the
+// other set of columns (`sets` of them; with one the next chain waits).  4.2e-7 with 16 MMAs
+// a chain, 7.8e-7 with 32, in the same time.
+constexpr int kChain = 4;
 
 template <int NS>
 struct Ring {

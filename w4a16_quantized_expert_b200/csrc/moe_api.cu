@@ -510,7 +510,7 @@ using namespace moe;
 
 extern "C" {
 
-int moe_version(void) { return 100; }
+int moe_version(void) { return 200; }
 
 const char *moe_status_string(int status)
 {

@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kRowThreads) unsort_grad_kernel(UnsortGradPara
             r = -1;
         }
     }
-    float dot = 0.f;
+    float dots[8] = {};   // (apart, so that no sum is a long chain)
     if (r >= 0) {
         const TD *dy = static_cast<const TD *>(p.dy) + (a / p.k) * p.lddy;
         const TR *row = static_cast<const TR *>(p.rows) + (size_t)r * p.H;
@@ -447,13 +447,14 @@ __global__ void __launch_bounds__(kRowThreads) unsort_grad_kernel(UnsortGradPara
                     to_f32(d[u], g);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        dot = fmaf(f[i], g[i], dot);
+                        dots[i] = fmaf(f[i], g[i], dots[i]);
                         g[i] = w == 0.f ? 0.f : w * g[i];   // weight 0: the forward pass skipped the row
                     }
                     store8(drow + b + u * step, pack8<TR>(g));
                 }
         }
     }
+    float dot = ((dots[0] + dots[1]) + (dots[2] + dots[3])) + ((dots[4] + dots[5]) + (dots[6] + dots[7]));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     if (kWarps > 1) {
