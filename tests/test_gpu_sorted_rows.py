@@ -430,10 +430,10 @@ def test_offsets_past_32_bits():
     assert status(L) == moe.MOE_OK
 
 
-@pytest.mark.parametrize("T,E,k", [(64, 256, 8), (65, 256, 8), (256, 16, 8), (257, 16, 8), (2048, 256, 8),
+@pytest.mark.parametrize("T,E,k", [(64, 256, 8), (128, 1024, 8), (129, 256, 8), (256, 16, 8), (257, 16, 8), (2048, 256, 8),
                                    (2049, 256, 8)])
 def test_sort_at_the_borders_of_its_paths(T, E, k):
-    """512 assignments (one launch), 2048 (one chunk) and 16384 (one cluster), and one token more."""
+    """1024 assignments (one launch), 2048 (one chunk) and 16384 (one cluster), and one token more."""
     H, align = 64, 4
     L = layer(H, E, k, T)
     idx = routing(T, E, k, T)

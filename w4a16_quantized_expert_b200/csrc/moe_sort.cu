@@ -250,9 +250,10 @@ __global__ void __launch_bounds__(kRowThreads) sort_copy_kernel(CopyParams p)
 
 // The sort and the copy of a decode-sized batch (at most kSmallSort assignments) in one
 // launch: every CTA counts all the keys itself (a few per thread), scans the counts and ranks
-// its own token's assignments, so that nothing waits for another CTA.  One token of 6144
-// fp16 and 8 of 256 experts: 3.6 us a call in a graph, two launches 4.3.
-constexpr int kSmallSort = 512;
+// its own token's assignments, so that nothing waits for another CTA.  Rows of 6144 bf16, 8 of
+// 256 experts, a call in a graph: 256 assignments 3.7 us (two launches 5.5), 1024 6.3 (8.0),
+// 2048 13.4 (12.7).
+constexpr int kSmallSort = 1024;
 
 __global__ void __launch_bounds__(kRowThreads) sort_small_kernel(SortParams s, CopyParams p)
 {
@@ -558,7 +559,9 @@ cudaError_t launch_unsort_grad(const void *dy, int dy_dtype, long long lddy, con
     p.n_rows = n_rows;
     p.status = status;
     const int n = T * k;
-    const bool few = n < 8 * 2 * num_sms;   // a CTA per assignment while warps would leave SMs idle
+    // a CTA per assignment while warps would leave SMs idle (rows of 6144 bf16: 296 assignments
+    // 2.6 us against 6.1, 2048 12.3 against 12.1, 3200 18.0 against 15.3)
+    const bool few = n < 8 * 2 * num_sms;
     p.n_blocks = few ? n : (n + kRowThreads / 32 - 1) / (kRowThreads / 32);
     const ChainLaunch l = {dim3(p.n_blocks + (seg ? E : 0)), kRowThreads, 0, 1, s};
     return by_type(rows_dtype, [&](auto tr) {
